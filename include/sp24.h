@@ -97,7 +97,8 @@ enum {
   SP24_ERR_ALIGN = 3,       /* a device pointer is not 16-byte aligned           */
   SP24_ERR_LAUNCH = 4,      /* the HIP runtime rejected a kernel launch          */
   SP24_ERR_UNSUPPORTED = 5, /* not available on this device / build              */
-  SP24_ERR_TOO_LARGE = 6    /* a size exceeds the kernels' index range           */
+  SP24_ERR_TOO_LARGE = 6,   /* a size exceeds the kernels' index range           */
+  SP24_ERR_WORKSPACE = 7    /* the workspace is smaller than the call needs      */
 };
 
 /*
@@ -418,6 +419,136 @@ int sp24_geglu_bwd(const void* U, const void* dout, int64_t T, int64_t h, int64_
  */
 int sp24_mvue(const void* M, const float* U, int64_t rows, int64_t cols, void* vals, uint16_t* meta,
               void* stream);
+
+/* Element types of the calls below that take more than one. */
+enum {
+  SP24_F16 = 0,
+  SP24_F32 = 1,
+  SP24_I32 = 2,
+  SP24_I64 = 3
+};
+
+/*
+ * Token embedding: out[t] = scale * table[ids[t]], rounded to nearest even in
+ * fp16.  It makes the FFN path's input from token ids.  An id outside [0, V)
+ * is padding and gives a row of zeros.
+ *
+ *   ids     in   [T], SP24_I32 or SP24_I64 (id_type)
+ *   table   in   [V, d], SP24_F16 or SP24_F32 (table_type)
+ *   T, V, d      >= 0, of any size (widths that are multiples of 8 are read
+ *                16 bytes at a time)
+ *   out     out  fp16 [T, d] (may not overlap the table)
+ * Errors: NULL (the table may be NULL when V is 0), SHAPE, ALIGN, LAUNCH;
+ * UNSUPPORTED for another type; TOO_LARGE when T, V or d reaches 2^31, a
+ * matrix 2^40 entries, or the output 2^34 chunks of 8 entries (of 1 entry
+ * where d is not a multiple of 8).
+ */
+int sp24_embed_fwd(const void* ids, int id_type, int64_t T, const void* table, int table_type, int64_t V, int64_t d,
+                   float scale, void* out, void* stream);
+
+/*
+ * Gradient of sp24_embed_fwd with respect to the table:
+ *   dtable[v] = scale * sum over t with ids[t] == v of dout[t]
+ * summed in fp32 in an order that the token positions fix (tokens of one id
+ * in order, in parts of up to 64), so the same inputs give the same bits.
+ * accumulate != 0 adds the sums to dtable, whose other rows are left as they
+ * are (a table tied to an output layer has a gradient there already);
+ * otherwise every row is written, those of absent ids with zeros.  Padding
+ * ids add nothing.
+ *
+ *   ids        in      [T], SP24_I32 or SP24_I64 (id_type)
+ *   dout       in      fp16 [T, d]
+ *   dtable     out     fp32 [V, d] (in/out with accumulate)
+ *   workspace  scratch device memory of sp24_embed_bwd_workspace bytes
+ * Errors: NULL, SHAPE, ALIGN, LAUNCH; UNSUPPORTED for another id type;
+ * WORKSPACE when workspace_bytes is too few; TOO_LARGE when T reaches 2^28, d
+ * 2^24, V 2^31, or a matrix 2^40 entries.
+ */
+int sp24_embed_bwd(const void* ids, int id_type, int64_t T, const void* dout, int64_t V, int64_t d, float scale,
+                   int accumulate, float* dtable, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
+
+/*
+ * Orthogonalises up to SP24_MAX_BATCH weight updates by Newton-Schulz
+ * products.  With X [m, n] the update G or its transpose, m <= n:
+ *   X_0 = G / (|G|_F + eps),   A = X X^T,   X <- a X + (b A + c A A) X
+ * `steps` times, each step with its own (a, b, c).  A step maps every
+ * singular value s to a s + b s^3 + c s^5 and leaves the singular vectors;
+ * the usual (3.4445, -4.7750, 2.0315), five times, brings all but the
+ * smallest to about 1.  A zero update gives zeros (for eps > 0).
+ *
+ * out_type SP24_F16: the products' operands are rounded to fp16 (at a scale
+ * that keeps their full precision); fp32 sums.  With the usual coefficients
+ * the result is within about 2e-3 of exact arithmetic, normwise.
+ * out_type SP24_F32: operands in two fp16 parts, three products each, for
+ * results to about fp32's own accuracy.
+ *
+ *   jobs       in    host array: G [R, C] of g_type, out [R, C] of out_type
+ *                    (may be G's own memory when the types agree)
+ *   coef       in    host array of 3 * steps floats: a, b, c of each step,
+ *                    such that no singular value passes 4 on the way
+ *   steps            1..SP24_MAX_NS_STEPS
+ *   eps              >= 0
+ *   workspace        device memory of sp24_orthogonalize_workspace bytes (the
+ *                    pointers in jobs do not matter to it)
+ * Errors: NULL, SHAPE (also count or steps out of range), ALIGN, LAUNCH;
+ * UNSUPPORTED for another type or a negative eps; WORKSPACE; TOO_LARGE when a
+ * job's (min(R, C) + 128) * (max(R, C) + 128) reaches 2^30.
+ */
+typedef struct sp24_ortho_job {
+  const void* G;
+  void* out;
+  int64_t R;
+  int64_t C;
+} sp24_ortho_job;
+
+#define SP24_MAX_NS_STEPS 32
+
+int sp24_orthogonalize(const sp24_ortho_job* jobs, int count, int g_type, int out_type, const float* coef, int steps,
+                       float eps, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_orthogonalize_workspace(const sp24_ortho_job* jobs, int count);
+
+/*
+ * One optimiser step of up to SP24_MAX_BATCH weights with momentum and an
+ * orthogonalised update (sp24_orthogonalize's), in place:
+ *   M <- momentum M + G
+ *   U  = G + momentum M if nesterov, else M
+ *   P <- (1 - decay) P - lr * orthogonalised U
+ *   W  = fp16(P)
+ * The last product's epilogue applies the update, so it is never written.
+ * sp24_weight_grad's dW is such a G; W is the weight that
+ * sp24_search_compress then searches.
+ *
+ *   jobs  in  host array, one per weight:
+ *     G       in      fp32 [R, C]
+ *     M, P    in/out  fp32 [R, C]
+ *     W       out     fp16 [R, C], or NULL
+ *     lr, decay       the update's factor (with any factor for the weight's
+ *                     shape) and the part of P that is taken off (lr times
+ *                     the weight decay)
+ *   precise != 0: products of two-part operands, as for SP24_F32 results
+ *   coef, steps, eps, workspace, errors: as sp24_orthogonalize
+ */
+typedef struct sp24_muon_job {
+  const float* G;
+  float* M;
+  float* P;
+  void* W;
+  int64_t R;
+  int64_t C;
+  float lr;
+  float decay;
+} sp24_muon_job;
+
+int sp24_muon_step(const sp24_muon_job* jobs, int count, float momentum, int nesterov, int precise, const float* coef,
+                   int steps, float eps, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_muon_workspace(const sp24_muon_job* jobs, int count);
 
 /* Host only: a static, human-readable name for a status code. */
 const char* sp24_status_str(int status);

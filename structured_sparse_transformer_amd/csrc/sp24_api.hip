@@ -93,6 +93,44 @@ int check_geglu(int64_t T, int64_t h, int64_t group) {
   return SP24_OK;
 }
 
+constexpr int64_t kMaxEmbedTokens = (int64_t)1 << 28, kMaxEmbedWidth = (int64_t)1 << 24;
+
+int check_embed_bwd(int64_t T, int64_t V, int64_t d) {
+  int st = check_dims(T, d, 1);
+  if (st != SP24_OK) return st;
+  if ((st = check_dims(V, d, 1)) != SP24_OK) return st;
+  return T >= kMaxEmbedTokens || d >= kMaxEmbedWidth ? SP24_ERR_TOO_LARGE : SP24_OK;
+}
+
+int check_ns_shape(int64_t R, int64_t C) {
+  const int st = check_dims(R, C, 1);
+  if (st != SP24_OK) return st;
+  // rows of tiles past the matrix's end still have 32-bit byte offsets
+  return R != 0 && C != 0 && R + 128 >= ((int64_t)1 << 30) / (C + 128) ? SP24_ERR_TOO_LARGE : SP24_OK;
+}
+
+int ns_params(const float* coef, int steps, float eps, sp24::NsParams& prm) {
+  static_assert(SP24_MAX_NS_STEPS == sp24::kMaxNsSteps && SP24_MAX_BATCH == sp24::kMaxNsJobs, "table sizes");
+  if (steps < 1 || steps > SP24_MAX_NS_STEPS) return SP24_ERR_SHAPE;
+  if (coef == nullptr) return SP24_ERR_NULL;
+  if (!(eps >= 0.0f)) return SP24_ERR_UNSUPPORTED;
+  prm.eps = eps;
+  prm.steps = steps;
+  for (int k = 0; k < 3 * steps; ++k) prm.coef[k] = coef[k];
+  return SP24_OK;
+}
+
+// Launches checked jobs.
+int ns_launch(const sp24::NsJob* d, int count, const sp24::NsParams& prm, void* workspace, int64_t workspace_bytes,
+              void* stream) {
+  const int64_t need = sp24::ns_workspace(d, count);
+  if (need == 0) return SP24_OK;
+  if (workspace == nullptr) return SP24_ERR_NULL;
+  if (!aligned16(workspace)) return SP24_ERR_ALIGN;
+  if (workspace_bytes < need) return SP24_ERR_WORKSPACE;
+  return launch_status(sp24::launch_newton_schulz(d, count, prm, workspace, as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -265,6 +303,119 @@ int sp24_mvue(const void* M, const float* U, int64_t rows, int64_t cols, void* v
                                          meta, as_stream(stream)));
 }
 
+int sp24_embed_fwd(const void* ids, int id_type, int64_t T, const void* table, int table_type, int64_t V, int64_t d,
+                   float scale, void* out, void* stream) {
+  if ((id_type != SP24_I32 && id_type != SP24_I64) || (table_type != SP24_F16 && table_type != SP24_F32))
+    return SP24_ERR_UNSUPPORTED;
+  int st = check_dims(T, d, 1);
+  if (st != SP24_OK) return st;
+  if ((st = check_dims(V, d, 1)) != SP24_OK) return st;
+  // a work-item takes four chunks of 8 entries, or of 1
+  if (T != 0 && (d % 8 == 0 ? d / 8 : d) > 4 * (kMaxLaunchItems - 256) / T) return SP24_ERR_TOO_LARGE;
+  if (T == 0 || d == 0) return SP24_OK;
+  if (ids == nullptr || out == nullptr || (V != 0 && table == nullptr)) return SP24_ERR_NULL;
+  if (!aligned16(ids) || !aligned16(out) || (V != 0 && !aligned16(table))) return SP24_ERR_ALIGN;
+  return launch_status(sp24::launch_embed_fwd(ids, id_type == SP24_I64, table, table_type == SP24_F32, T, V, d, scale,
+                                              static_cast<uint16_t*>(out), as_stream(stream)));
+}
+
+int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d) {
+  return check_embed_bwd(T, V, d) == SP24_OK ? sp24::embed_bwd_workspace(T, V, d) : -1;
+}
+
+int sp24_embed_bwd(const void* ids, int id_type, int64_t T, const void* dout, int64_t V, int64_t d, float scale,
+                   int accumulate, float* dtable, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (id_type != SP24_I32 && id_type != SP24_I64) return SP24_ERR_UNSUPPORTED;
+  const int st = check_embed_bwd(T, V, d);
+  if (st != SP24_OK) return st;
+  if (V == 0 || d == 0 || (T == 0 && accumulate)) return SP24_OK;
+  if (dtable == nullptr || workspace == nullptr || (T != 0 && (ids == nullptr || dout == nullptr))) return SP24_ERR_NULL;
+  if (!aligned16(dtable) || !aligned16(workspace) || (T != 0 && (!aligned16(ids) || !aligned16(dout))))
+    return SP24_ERR_ALIGN;
+  if (workspace_bytes < sp24::embed_bwd_workspace(T, V, d)) return SP24_ERR_WORKSPACE;
+  return launch_status(sp24::launch_embed_bwd(ids, id_type == SP24_I64, T, static_cast<const uint16_t*>(dout), V, d,
+                                              scale, accumulate != 0, dtable, workspace, as_stream(stream)));
+}
+
+int64_t sp24_orthogonalize_workspace(const sp24_ortho_job* jobs, int count) {
+  if (jobs == nullptr || count < 1 || count > SP24_MAX_BATCH) return -1;
+  sp24::NsJob d[SP24_MAX_BATCH] = {};
+  for (int k = 0; k < count; ++k) {
+    if (check_ns_shape(jobs[k].R, jobs[k].C) != SP24_OK) return -1;
+    d[k].R = jobs[k].R;
+    d[k].C = jobs[k].C;
+  }
+  return sp24::ns_workspace(d, count);
+}
+
+int sp24_orthogonalize(const sp24_ortho_job* jobs, int count, int g_type, int out_type, const float* coef, int steps,
+                       float eps, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (jobs == nullptr) return SP24_ERR_NULL;
+  if (count < 1 || count > SP24_MAX_BATCH) return SP24_ERR_SHAPE;
+  if ((g_type != SP24_F16 && g_type != SP24_F32) || (out_type != SP24_F16 && out_type != SP24_F32))
+    return SP24_ERR_UNSUPPORTED;
+  sp24::NsParams prm{};
+  int st = ns_params(coef, steps, eps, prm);
+  if (st != SP24_OK) return st;
+  prm.split = out_type == SP24_F32;
+  sp24::NsJob d[SP24_MAX_BATCH] = {};
+  for (int k = 0; k < count; ++k) {
+    const sp24_ortho_job& j = jobs[k];
+    if ((st = check_ns_shape(j.R, j.C)) != SP24_OK) return st;
+    d[k].R = j.R;
+    d[k].C = j.C;
+    if (j.R == 0 || j.C == 0) continue;
+    if (j.G == nullptr || j.out == nullptr) return SP24_ERR_NULL;
+    if (!aligned16(j.G) || !aligned16(j.out)) return SP24_ERR_ALIGN;
+    d[k].G = j.G;
+    d[k].g32 = g_type == SP24_F32;
+    d[k].out = j.out;
+    d[k].out32 = out_type == SP24_F32;
+  }
+  return ns_launch(d, count, prm, workspace, workspace_bytes, stream);
+}
+
+int64_t sp24_muon_workspace(const sp24_muon_job* jobs, int count) {
+  if (jobs == nullptr || count < 1 || count > SP24_MAX_BATCH) return -1;
+  sp24::NsJob d[SP24_MAX_BATCH] = {};
+  for (int k = 0; k < count; ++k) {
+    if (check_ns_shape(jobs[k].R, jobs[k].C) != SP24_OK) return -1;
+    d[k].R = jobs[k].R;
+    d[k].C = jobs[k].C;
+  }
+  return sp24::ns_workspace(d, count);
+}
+
+int sp24_muon_step(const sp24_muon_job* jobs, int count, float momentum, int nesterov, int precise, const float* coef,
+                   int steps, float eps, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (jobs == nullptr) return SP24_ERR_NULL;
+  if (count < 1 || count > SP24_MAX_BATCH) return SP24_ERR_SHAPE;
+  sp24::NsParams prm{};
+  int st = ns_params(coef, steps, eps, prm);
+  if (st != SP24_OK) return st;
+  prm.mu = momentum;
+  prm.nesterov = nesterov != 0;
+  prm.split = precise != 0;
+  sp24::NsJob d[SP24_MAX_BATCH] = {};
+  for (int k = 0; k < count; ++k) {
+    const sp24_muon_job& j = jobs[k];
+    if ((st = check_ns_shape(j.R, j.C)) != SP24_OK) return st;
+    d[k].R = j.R;
+    d[k].C = j.C;
+    if (j.R == 0 || j.C == 0) continue;
+    if (j.G == nullptr || j.M == nullptr || j.P == nullptr) return SP24_ERR_NULL;
+    if (!aligned16(j.G) || !aligned16(j.M) || !aligned16(j.P) || (j.W && !aligned16(j.W))) return SP24_ERR_ALIGN;
+    d[k].G = j.G;
+    d[k].g32 = true;
+    d[k].M = j.M;
+    d[k].P = j.P;
+    d[k].W = static_cast<uint16_t*>(j.W);
+    d[k].lr = j.lr;
+    d[k].keep = 1.0f - j.decay;
+  }
+  return ns_launch(d, count, prm, workspace, workspace_bytes, stream);
+}
+
 const char* sp24_status_str(int status) {
   switch (status) {
     case SP24_OK: return "ok";
@@ -274,6 +425,7 @@ const char* sp24_status_str(int status) {
     case SP24_ERR_LAUNCH: return "kernel launch failed";
     case SP24_ERR_UNSUPPORTED: return "unsupported";
     case SP24_ERR_TOO_LARGE: return "size exceeds index range";
+    case SP24_ERR_WORKSPACE: return "workspace too small";
     default: return "unknown status";
   }
 }

@@ -107,4 +107,40 @@ hipError_t launch_spmm_group(const GemmDesc* jobs, int count, unsigned int* work
 constexpr int kGroupScratchWords = 16;
 hipError_t group_scratch(unsigned int** out);
 
+// out[T][d] (fp16) = scale * table[ids[t]], zero rows for ids outside [0, V).
+// ids int64 or int32; table fp32 or fp16 [V][d].  T, d > 0.
+hipError_t launch_embed_fwd(const void* ids, bool ids64, const void* table, bool table32, int64_t T, int64_t V, int64_t d,
+                            float scale, uint16_t* out, hipStream_t s);
+// dtable[V][d] (fp32) = (add: dtable +) scale * the sums of dout's rows by id.
+// V, d > 0.  ws: embed_bwd_workspace bytes of device memory.
+int64_t embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
+hipError_t launch_embed_bwd(const void* ids, bool ids64, int64_t T, const uint16_t* dout, int64_t V, int64_t d,
+                            float scale, bool add, float* dtable, void* ws, hipStream_t s);
+
+// One weight of a Newton-Schulz launch: its update is U = G, or with
+// momentum M <- mu M + G, U = G + mu M (nesterov) or M.  Results: the
+// orthogonalised update in out, or P <- keep P - lr X and W = fp16(P).
+struct NsJob {
+  const void* G;       // [R][C]; fp16 if !g32
+  bool g32;
+  int64_t R, C;
+  float* M;            // momentum, or nullptr
+  void* out;           // [R][C]; fp16 if !out32; nullptr with P
+  bool out32;
+  float* P;            // fp32 weights, or nullptr
+  uint16_t* W;         // their fp16 copy, or nullptr
+  float lr, keep;
+};
+constexpr int kMaxNsJobs = 8, kMaxNsSteps = 32;
+struct NsParams {
+  float mu, eps;
+  bool nesterov;
+  bool split;          // products of two-part operands, to fp32 accuracy
+  int steps;
+  float coef[3 * kMaxNsSteps];
+};
+// Workspace bytes of a launch over these jobs (their R and C alone matter).
+int64_t ns_workspace(const NsJob* jobs, int count);
+hipError_t launch_newton_schulz(const NsJob* jobs, int count, const NsParams& prm, void* ws, hipStream_t s);
+
 }  // namespace sp24

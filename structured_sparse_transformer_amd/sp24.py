@@ -16,6 +16,7 @@ of such a tensor is not a row of the form.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -26,15 +27,22 @@ LIB_PATH = os.path.join(_HERE, "libsp24.so")
 
 SP24_OK = 0
 STATUS_NAMES = {0: "OK", 1: "ERR_NULL", 2: "ERR_SHAPE", 3: "ERR_ALIGN", 4: "ERR_LAUNCH",
-                5: "ERR_UNSUPPORTED", 6: "ERR_TOO_LARGE"}
+                5: "ERR_UNSUPPORTED", 6: "ERR_TOO_LARGE", 7: "ERR_WORKSPACE"}
 EXPORTS = ("sp24_mask_search", "sp24_compress", "sp24_search_compress", "sp24_search_compress_batch",
            "sp24_flip_count", "sp24_weight_grad", "sp24_geglu_fwd", "sp24_geglu_bwd", "sp24_mvue",
            "sp24_spmm_fwd", "sp24_spmm_fwd_geglu", "sp24_spmm_bwd_input", "sp24_spmm_group",
-           "sp24_spmm_group_noalloc", "sp24_status_str",
+           "sp24_spmm_group_noalloc", "sp24_embed_fwd", "sp24_embed_bwd", "sp24_embed_bwd_workspace",
+           "sp24_orthogonalize", "sp24_orthogonalize_workspace", "sp24_muon_step", "sp24_muon_workspace",
+           "sp24_status_str",
            "sp24_pattern_table", "sp24_abi_version")
 MAX_BATCH = 8
 MAX_GROUP = 8
 GROUP_WORKSPACE_BYTES = 64
+MAX_NS_STEPS = 32
+F16, F32, I32, I64 = 0, 1, 2, 3
+# the usual quintic of the Newton-Schulz iteration: five steps bring singular
+# values to about [0.7, 1.2]
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
 class ScJob(ctypes.Structure):
@@ -49,6 +57,17 @@ class Gemm(ctypes.Structure):
     """Mirror of sp24_gemm (include/sp24.h)."""
     _fields_ = [("A", ctypes.c_void_p), ("vals", ctypes.c_void_p), ("meta", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("T", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class OrthoJob(ctypes.Structure):
+    """Mirror of sp24_ortho_job (include/sp24.h)."""
+    _fields_ = [("G", ctypes.c_void_p), ("out", ctypes.c_void_p), ("R", ctypes.c_int64), ("C", ctypes.c_int64)]
+
+
+class MuonJob(ctypes.Structure):
+    """Mirror of sp24_muon_job (include/sp24.h)."""
+    _fields_ = [("G", ctypes.c_void_p), ("M", ctypes.c_void_p), ("P", ctypes.c_void_p), ("W", ctypes.c_void_p),
+                ("R", ctypes.c_int64), ("C", ctypes.c_int64), ("lr", ctypes.c_float), ("decay", ctypes.c_float)]
 
 
 class Sp24Error(RuntimeError):
@@ -83,6 +102,13 @@ def lib() -> ctypes.CDLL:
             "sp24_spmm_bwd_input": [p, p, p, i64, i64, i64, p, p],
             "sp24_spmm_group": [p, i32, p, p],
             "sp24_spmm_group_noalloc": [p, i32, p],
+            "sp24_embed_fwd": [p, i32, i64, p, i32, i64, i64, ctypes.c_float, p, p],
+            "sp24_embed_bwd": [p, i32, i64, p, i64, i64, ctypes.c_float, i32, p, p, i64, p],
+            "sp24_embed_bwd_workspace": [i64, i64, i64],
+            "sp24_orthogonalize": [p, i32, i32, i32, p, i32, ctypes.c_float, p, i64, p],
+            "sp24_orthogonalize_workspace": [p, i32],
+            "sp24_muon_step": [p, i32, ctypes.c_float, i32, i32, p, i32, ctypes.c_float, p, i64, p],
+            "sp24_muon_workspace": [p, i32],
             "sp24_status_str": [i32],
             "sp24_pattern_table": [p],
             "sp24_abi_version": [],
@@ -90,7 +116,8 @@ def lib() -> ctypes.CDLL:
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes = args
-            f.restype = ctypes.c_char_p if name == "sp24_status_str" else i32
+            f.restype = (ctypes.c_char_p if name == "sp24_status_str" else
+                         i64 if name.endswith("_workspace") else i32)
         _lib = L
     return _lib
 
@@ -419,3 +446,143 @@ def sp24_spmm_group(gemms, workspace=None, stream=None):
     _check("sp24_spmm_group", lib().sp24_spmm_group(ctypes.cast(descs, ctypes.c_void_p), len(gemms), _ptr(ws),
                                                     _stream(stream)))
     return outs
+
+
+def _id_type(ids):
+    types = {torch.int32: I32, torch.int64: I64}
+    if ids.dtype not in types:
+        raise ValueError("ids must be int32 or int64")
+    return types[ids.dtype]
+
+
+def _using(stream):
+    """What is allocated within belongs to the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace(t, need, device):
+    """The caller's workspace, or one of `need` bytes."""
+    if need < 0:
+        raise ValueError("the sizes are beyond what the call takes")
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if t.numel() * t.element_size() < need:
+        raise ValueError(f"the workspace needs {need} bytes")
+    return t
+
+
+def sp24_embed_fwd(ids, table, scale=1.0, out=None, stream=None):
+    """out [*ids.shape, d] (float16) = scale * table[ids]; rows of ids outside
+    [0, V) are zeros.  ids int32 or int64, table float16 or float32 [V, d]."""
+    types = {torch.float16: F16, torch.float32: F32}
+    if table.dtype not in types or table.dim() != 2:
+        raise ValueError("the table must be a 2-D float16 or float32 tensor")
+    kind = _id_type(ids)
+    V, d = table.shape
+    with _using(stream):
+        out = _out(out, (*ids.shape, d), torch.float16, table.device)
+    _check("sp24_embed_fwd", lib().sp24_embed_fwd(_ptr(ids), kind, ids.numel(), _ptr(table), types[table.dtype], V, d,
+                                                  float(scale), _ptr(out), _stream(stream)))
+    return out
+
+
+def sp24_embed_bwd_workspace(T, V, d):
+    """Bytes of sp24_embed_bwd's workspace."""
+    return lib().sp24_embed_bwd_workspace(T, V, d)
+
+
+def sp24_embed_bwd(ids, dout, V, scale=1.0, dtable=None, accumulate=False, workspace=None, stream=None):
+    """dtable [V, d] (float32): scale times the sums of dout's rows by id, in
+    token order.  ``accumulate`` adds them to the ``dtable`` given."""
+    kind = _id_type(ids)
+    if dout.dtype != torch.float16 or dout.dim() != ids.dim() + 1 or dout.shape[:-1] != ids.shape:
+        raise ValueError("dout must be float16 [*ids.shape, d]")
+    if accumulate and dtable is None:
+        raise ValueError("accumulate needs the dtable to add to")
+    if V < 0:
+        raise ValueError("V must not be negative")
+    T, d = ids.numel(), dout.shape[-1]
+    with _using(stream):
+        dtable = _out(dtable, (V, d), torch.float32, dout.device)
+        workspace = _workspace(workspace, sp24_embed_bwd_workspace(T, V, d), dout.device)
+    _check("sp24_embed_bwd", lib().sp24_embed_bwd(
+        _ptr(ids), kind, T, _ptr(dout), V, d, float(scale), int(bool(accumulate)), _ptr(dtable), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dtable
+
+
+def _coeffs(coeffs, steps):
+    """The (a, b, c) of every step: one triple for all of them, or one each."""
+    if not 1 <= steps <= MAX_NS_STEPS:
+        raise ValueError(f"between 1 and {MAX_NS_STEPS} steps")
+    rows = list(NS_COEFFS if coeffs is None else coeffs)
+    rows = [rows] * steps if not hasattr(rows[0], "__len__") else [list(r) for r in rows]
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coeffs must be (a, b, c), or one such triple per step")
+    return (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+
+
+def sp24_orthogonalize_batch(Gs, steps=5, coeffs=None, eps=1e-7, dtype=torch.float16, outs=None, workspace=None,
+                             stream=None):
+    """The orthogonalised updates of up to 8 weights (all float16 or all
+    float32, [R, C] each) by `steps` Newton-Schulz steps, in one sequence of
+    launches.  ``dtype`` float16: products of fp16 operands; float32: to
+    float32's accuracy, at about three times the work."""
+    if not 1 <= len(Gs) <= MAX_BATCH:
+        raise ValueError(f"between 1 and {MAX_BATCH} updates per batch")
+    types = {torch.float16: F16, torch.float32: F32}
+    if dtype not in types or any(G.dtype not in types or G.dtype != Gs[0].dtype or G.dim() != 2 for G in Gs):
+        raise ValueError("updates must be 2-D float16 or float32 tensors of one type, dtype one of the two")
+    coef = _coeffs(coeffs, steps)
+    if outs is not None and len(outs) != len(Gs):
+        raise ValueError("outs needs one entry per update")
+    res, jobs = [], (OrthoJob * len(Gs))()
+    for k, G in enumerate(Gs):
+        with _using(stream):
+            out = _out(outs[k] if outs is not None else None, G.shape, dtype, G.device)
+        ptr = lambda t: _ptr(t).value if t.numel() else None  # noqa: E731
+        jobs[k] = OrthoJob(ptr(G), ptr(out), G.shape[0], G.shape[1])
+        res.append(out)
+    arr = ctypes.cast(jobs, ctypes.c_void_p)
+    with _using(stream):
+        workspace = _workspace(workspace, lib().sp24_orthogonalize_workspace(arr, len(Gs)), Gs[0].device)
+    _check("sp24_orthogonalize", lib().sp24_orthogonalize(
+        arr, len(Gs), types[Gs[0].dtype], types[dtype], ctypes.cast(coef, ctypes.c_void_p), steps, float(eps),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return res
+
+
+def sp24_orthogonalize(G, steps=5, coeffs=None, eps=1e-7, dtype=torch.float16, out=None, workspace=None, stream=None):
+    """sp24_orthogonalize_batch of one update."""
+    return sp24_orthogonalize_batch([G], steps, coeffs, eps, dtype, None if out is None else [out], workspace, stream)[0]
+
+
+def sp24_muon_step(Gs, Ms, Ps, Ws, lrs, decays=None, momentum=0.95, nesterov=True, steps=5, coeffs=None, eps=1e-7,
+                   precise=False, workspace=None, stream=None):
+    """One optimiser step of up to 8 weights, in place: momentum Ms[k] and
+    weights Ps[k] (float32 [R, C]) from the gradient Gs[k] (float32), and
+    Ws[k] (float16, or None) = Ps[k].  lrs[k] multiplies the orthogonalised
+    update, 1 - decays[k] the weight."""
+    n = len(Gs)
+    if not 1 <= n <= MAX_BATCH:
+        raise ValueError(f"between 1 and {MAX_BATCH} weights per step")
+    decays = [0.0] * n if decays is None else decays
+    if any(len(v) != n for v in (Ms, Ps, Ws, lrs, decays)):
+        raise ValueError("Ms, Ps, Ws, lrs and decays need one entry per gradient")
+    coef = _coeffs(coeffs, steps)
+    jobs = (MuonJob * n)()
+    ptr = lambda t: _ptr(t).value if t is not None and t.numel() else None  # noqa: E731
+    for k, (G, M, P, W) in enumerate(zip(Gs, Ms, Ps, Ws)):
+        if G.dtype != torch.float32 or G.dim() != 2:
+            raise ValueError("gradients must be 2-D float32 tensors")
+        _need(M, G.shape, torch.float32, "the momentum")
+        _need(P, G.shape, torch.float32, "the weight")
+        if W is not None:
+            _need(W, G.shape, torch.float16, "the float16 weight")
+        jobs[k] = MuonJob(ptr(G), ptr(M), ptr(P), ptr(W), G.shape[0], G.shape[1], float(lrs[k]), float(decays[k]))
+    arr = ctypes.cast(jobs, ctypes.c_void_p)
+    with _using(stream):
+        workspace = _workspace(workspace, lib().sp24_muon_workspace(arr, n), Gs[0].device)
+    _check("sp24_muon_step", lib().sp24_muon_step(
+        arr, n, float(momentum), int(bool(nesterov)), int(bool(precise)), ctypes.cast(coef, ctypes.c_void_p), steps,
+        float(eps), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
