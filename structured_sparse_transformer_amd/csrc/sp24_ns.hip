@@ -51,7 +51,8 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 constexpr int kThreads = 256;
 constexpr float kScale = 4096.0f, kInvScale = 1.0f / 4096.0f;   // the units of X, A and B
 constexpr int kLoSteps = 3;
-constexpr int kNormBlocks = 256;   // partial sums of squares per weight
+constexpr int kNormChunk = 16 * kThreads;   // entries a workgroup squares at a time
+constexpr int kMaxParts = 1024;             // partial sums of squares per weight
 constexpr int kTile = 128;         // square tiles of the products
 constexpr int kBK = 32;            // reduction per stage
 
@@ -67,7 +68,8 @@ struct Job {
   int lda, ldx;    // row lengths of A, B and of X, multiples of 64
   bool tall;       // X is U^T
   bool g32, out32;
-  double* sums;                  // kNormBlocks
+  double* sums;                  // of squares, `parts` of them
+  int parts;
   _Float16* x[2];                // X, hi then lo part, before and after a step
   _Float16 *A, *B;               // hi then lo part
   int first;                     // first workgroup of the launch at hand
@@ -85,6 +87,41 @@ __device__ __forceinline__ const Job& job_of(const Jobs& jobs, int block) {
 
 __device__ __forceinline__ float load_g(const Job& j, int64_t i) {
   return j.g32 ? static_cast<const float*>(j.G)[i] : (float)static_cast<const _Float16*>(j.G)[i];
+}
+
+// Entries i .. i + 7 of a matrix of `total`; zeros past its end.  i is a
+// multiple of 8 and matrices start 16-byte aligned.
+__device__ __forceinline__ void load8(const void* p, bool is32, int64_t i, int64_t total, float (&v)[8]) {
+  if (i + 8 <= total) {
+    if (is32) {
+      const f4* q = reinterpret_cast<const f4*>(static_cast<const float*>(p) + i);
+      const f4 x = q[0], y = q[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = x[e];
+        v[4 + e] = y[e];
+      }
+    } else {
+      const h8 x = *reinterpret_cast<const h8*>(static_cast<const _Float16*>(p) + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = i + e >= total ? 0.0f : is32 ? static_cast<const float*>(p)[i + e] : (float)static_cast<const _Float16*>(p)[i + e];
+  }
+}
+__device__ __forceinline__ void store8(float* p, int64_t i, int64_t total, const float (&v)[8]) {
+  if (i + 8 <= total) {
+    f4* q = reinterpret_cast<f4*>(p + i);
+    q[0] = f4{v[0], v[1], v[2], v[3]};
+    q[1] = f4{v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < total) p[i + e] = v[e];
+  }
 }
 
 // The update of entry i from its gradient and its new momentum.
@@ -108,20 +145,34 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // Momentum, and the squares of the update summed in 64 bits (a sum of fp32
-// squares would lose updates below 1e-22 or above 1e19).
+// squares would lose updates below 1e-22 or above 1e19).  Eight entries a
+// thread at a time; a workgroup takes kNormChunk of them.
 __global__ __launch_bounds__(kThreads) void ns_norm_kernel(Jobs jobs, float mu, bool nesterov) {
   const Job& j = job_of(jobs, blockIdx.x);
   const int block = blockIdx.x - j.first;
   const int64_t total = (int64_t)j.m * j.n;
   double sum = 0.0;
-  for (int64_t i = (int64_t)block * kThreads + threadIdx.x; i < total; i += kNormBlocks * kThreads) {
-    float u = load_g(j, i);
-    if (j.M != nullptr) {
-      const float m = mu * j.M[i] + u;
-      j.M[i] = m;
-      u = nesterov ? u + mu * m : m;
+  for (int64_t base = (int64_t)block * kNormChunk; base < total; base += (int64_t)j.parts * kNormChunk) {
+    float u[2][8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t i = base + (q * kThreads + threadIdx.x) * 8;
+      load8(j.G, j.g32, i, total, u[q]);
+      if (j.M != nullptr) {
+        float m[8];
+        load8(j.M, true, i, total, m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          m[e] = mu * m[e] + u[q][e];
+          u[q][e] = nesterov ? u[q][e] + mu * m[e] : m[e];
+        }
+        store8(j.M, i, total, m);
+      }
     }
-    sum += (double)u * (double)u;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += (double)u[q][e] * (double)u[q][e];
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) j.sums[block] = sum;
@@ -140,7 +191,9 @@ __global__ __launch_bounds__(kThreads) void ns_start_kernel(Jobs jobs, float mu,
   const Job& j = job_of(jobs, blockIdx.x);
   const int block = blockIdx.x - j.first, tiles_n = j.ldx / 64;
   const int i0 = block / tiles_n * 64, j0 = block % tiles_n * 64;
-  const double norm = sqrt(block_sum(j.sums[threadIdx.x]));
+  double sum = 0.0;
+  for (int k = threadIdx.x; k < j.parts; k += kThreads) sum += j.sums[k];
+  const double norm = sqrt(block_sum(sum));
   const double scale = (double)kScale / (norm + (double)eps);
   const int64_t plane = (int64_t)j.m * j.ldx;
   if (j.tall) {
@@ -173,6 +226,81 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// What one lane of a wave has written to LDS is read by the others.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Eight values in their fp16 parts; 16-byte aligned.
+__device__ __forceinline__ void put8(_Float16* p, int64_t plane, bool both, const float (&v)[8]) {
+  h8 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    _Float16 h, l;
+    split(v[e], h, l);
+    hi[e] = h;
+    lo[e] = l;
+  }
+  *reinterpret_cast<h8*>(p) = hi;
+  if (both) *reinterpret_cast<h8*>(p + plane) = lo;
+}
+
+// Entries at .. at + 7 of a result's row of n, which starts at entry `row`:
+// the orthogonalised update, or the weight's step by it.
+__device__ __forceinline__ void finish8(const Job& j, int64_t row, int at, int n, const float (&v)[8]) {
+  const bool whole = at + 8 <= n && n % 8 == 0;   // rows start 16-byte aligned
+  const int64_t o = row + at;
+  if (j.P != nullptr) {
+    float p[8];
+    if (whole) {
+      load8(j.P, true, o, o + 8, p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = j.keep * p[e] - j.lr * v[e];
+      store8(j.P, o, o + 8, p);
+      if (j.W != nullptr) {
+        h8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (_Float16)p[e];
+        *reinterpret_cast<h8*>(j.W + o) = h;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = at + e < n ? j.P[o + e] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (at + e >= n) continue;
+        p[e] = j.keep * p[e] - j.lr * v[e];
+        j.P[o + e] = p[e];
+        if (j.W != nullptr) j.W[o + e] = __builtin_bit_cast(uint16_t, (_Float16)p[e]);
+      }
+    }
+    return;
+  }
+  if (j.out32) {
+    float* out = static_cast<float*>(j.out);
+    if (whole) {
+      store8(out, o, o + 8, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (at + e < n) out[o + e] = v[e];
+    }
+  } else {
+    _Float16* out = static_cast<_Float16*>(j.out);
+    if (whole) {
+      h8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
+      *reinterpret_cast<h8*>(out + o) = h;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (at + e < n) out[o + e] = (_Float16)v[e];
+    }
+  }
+}
+
 enum : int { kGram = 0, kPoly = 1, kApply = 2 };
 
 // The products' LDS stage: kTile rows x kBK of the left operand, then the
@@ -185,6 +313,8 @@ enum : int { kGram = 0, kPoly = 1, kApply = 2 };
 // fetches from four rows in different banks.
 constexpr int kOperand = kTile * kBK * 2;   // bytes of one operand's part
 constexpr int kRing = 3;
+constexpr int kTurn = 68;   // floats in a row of the epilogue's 32 x 64 blocks
+static_assert(4 * 32 * kTurn * 4 <= kRing * 2 * kOperand, "the epilogue's blocks fit the ring");
 
 template <int KIND, bool SPLIT, bool LAST>
 __global__ __launch_bounds__(kThreads) void ns_product_kernel(Jobs jobs, int cur, float a, float b, float c, bool use_lo) {
@@ -197,8 +327,13 @@ __global__ __launch_bounds__(kThreads) void ns_product_kernel(Jobs jobs, int cur
   const int tiles_m = (j.m + kTile - 1) / kTile;
   int tm, tn;
   if constexpr (KIND == kApply) {
-    tm = block % tiles_m;
-    tn = block / tiles_m;
+    // workgroups go round the 8 XCDs: each takes a run of column strips, whose
+    // X its L2 then fetches once
+    const int tiles = tiles_m * ((j.n + kTile - 1) / kTile), run = (tiles + 7) / 8;
+    const int lin = block % 8 * run + block / 8;
+    if (block / 8 >= run || lin >= tiles) return;
+    tm = lin % tiles_m;
+    tn = lin / tiles_m;
   } else {
     // row tm of the upper triangle holds tiles_m - tm tiles
     tm = 0;
@@ -327,79 +462,89 @@ __global__ __launch_bounds__(kThreads) void ns_product_kernel(Jobs jobs, int cur
     asm volatile("" ::: "memory");
   }
 
-  // Epilogue: four accumulators are rows r4 .. r4 + 3 of one column.
+  // Epilogue.  A wave turns 32 rows x 64 columns of accumulators at a time
+  // through its quarter of the ring, so that a lane holds 8 columns of a row:
+  // what it reads and writes there is whole 16-byte pieces of 128-byte runs.
+  // Results that go out transposed (the mirrored tile, a tall weight) are put
+  // back and read again by columns.  The loads of a block are issued before
+  // its first store.
+  __syncthreads();   // the ring is idle
+  float* const turn = reinterpret_cast<float*>(smem) + wave * (32 * kTurn);
+  const int er = lane >> 3, ec = (lane & 7) * 8;   // row (of 8) and first column
+  constexpr bool kLoads = KIND != kGram;
+  const bool back = KIND == kApply ? LAST && j.tall : tm != tn;
+  // what is read, and what is written: X, or A and B, of one shape
+  const _Float16* const old = KIND == kApply ? X : j.A;
+  _Float16* const D = KIND == kGram ? j.A : KIND == kPoly ? j.B : j.x[1 - cur];
+  const int64_t plane = KIND == kApply ? xplane : aplane;
+  const int ld = KIND == kApply ? j.ldx : j.lda;
+  const bool old_lo = SPLIT || (KIND == kApply && use_lo);
+  const int c0 = n0 + wn * 64 + ec;
+  const bool col_in = c0 < ld;
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+  for (int s = 0; s < 2; ++s) {
+    const int r0 = m0 + wm * 64 + s * 32;
+    h8 ohi[4], olo[4];
+    if constexpr (kLoads) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int col = n0 + wn * 64 + t * 32 + l32;
-#pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        const int r4 = m0 + wm * 64 + s * 32 + 8 * i4 + 4 * g;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[s][t][4 * i4 + e] * kInvScale;
-        if constexpr (KIND != kApply) {
-          if (col >= j.lda) continue;
-          _Float16* const D = KIND == kGram ? j.A : j.B;
-          h4 hi, lo;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int64_t at = (int64_t)(r4 + e) * j.lda + col;
-            if constexpr (KIND == kPoly) {
-              float p = 0.0f;
-              if (r4 + e < j.m) {
-                p = (float)j.A[at];
-                if constexpr (SPLIT) p += (float)j.A[aplane + at];
-              }
-              v[e] = b * p + c * v[e];
-            }
-            _Float16 h, l;
-            split(v[e], h, l);
-            hi[e] = h;
-            lo[e] = l;
-            if (r4 + e < j.m) {
-              D[at] = h;
-              if constexpr (SPLIT) D[aplane + at] = l;
-            }
-          }
-          // the mirrored tile: these four are consecutive in row col
-          if (tm != tn && col < j.m) {
-            const int64_t at = (int64_t)col * j.lda + r4;
-            *reinterpret_cast<h4*>(D + at) = hi;
-            if constexpr (SPLIT) *reinterpret_cast<h4*>(D + aplane + at) = lo;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = r4 + e;
-            if (row >= j.m || col >= (LAST ? j.n : j.ldx)) continue;
-            const int64_t at = (int64_t)row * j.ldx + col;
-            float x = (float)X[at];
-            if (SPLIT || use_lo) x += (float)X[xplane + at];
-            x = a * x + v[e];
-            if constexpr (!LAST) {
-              _Float16 h, l;
-              split(x, h, l);
-              j.x[1 - cur][at] = h;
-              j.x[1 - cur][xplane + at] = l;
-            } else {
-              x *= kInvScale;
-              const int64_t o = j.tall ? (int64_t)col * j.m + row : (int64_t)row * j.n + col;
-              if (j.P != nullptr) {
-                const float p = j.keep * j.P[o] - j.lr * x;
-                j.P[o] = p;
-                if (j.W != nullptr) j.W[o] = __builtin_bit_cast(uint16_t, (_Float16)p);
-              } else if (j.out32) {
-                static_cast<float*>(j.out)[o] = x;
-              } else {
-                static_cast<_Float16*>(j.out)[o] = (_Float16)x;
-              }
-            }
-          }
+      for (int p = 0; p < 4; ++p) {
+        const int row = r0 + p * 8 + er;
+        ohi[p] = olo[p] = h8{};
+        if (row < j.m && col_in) {
+          const _Float16* at = old + (int64_t)row * ld + c0;
+          ohi[p] = *reinterpret_cast<const h8*>(at);
+          if (old_lo) olo[p] = *reinterpret_cast<const h8*>(at + plane);
         }
       }
     }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) turn[(8 * (i >> 2) + 4 * g + (i & 3)) * kTurn + t * 32 + l32] = acc[s][t][i];
+    wave_sync();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int row = r0 + p * 8 + er;
+      float* const mine = turn + (p * 8 + er) * kTurn + ec;
+      const f4 v0 = *reinterpret_cast<const f4*>(mine), v1 = *reinterpret_cast<const f4*>(mine + 4);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = (e < 4 ? v0[e & 3] : v1[e & 3]) * kInvScale;
+        if constexpr (kLoads) {
+          const float o = (float)ohi[p][e] + (float)olo[p][e];
+          v[e] = KIND == kPoly ? b * o + c * v[e] : a * o + v[e];
+        }
+      }
+      if constexpr (KIND != kApply || !LAST) {
+        if (row < j.m && col_in) put8(D + (int64_t)row * ld + c0, plane, KIND == kApply || SPLIT, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= kInvScale;
+        if (!j.tall && row < j.m) finish8(j, (int64_t)row * j.n, c0, j.n, v);
+      }
+      if (back) {
+        *reinterpret_cast<f4*>(mine) = f4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f4*>(mine + 4) = f4{v[4], v[5], v[6], v[7]};
+      }
+    }
+    if (back) {
+      wave_sync();
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int cc = p * 16 + (lane >> 2), rr = (lane & 3) * 8, col = n0 + wn * 64 + cc, row = r0 + rr;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = turn[(rr + e) * kTurn + cc];
+        if constexpr (KIND != kApply) {
+          if (col < j.m) put8(D + (int64_t)col * ld + row, plane, SPLIT, v);
+        } else if constexpr (LAST) {
+          if (col < j.n) finish8(j, (int64_t)col * j.m, row, j.m, v);
+        }
+      }
+    }
+    wave_sync();   // the block has been read
+  }
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -413,7 +558,7 @@ int64_t lay_out(Job& j, unsigned char* base) {
     return p;
   };
   const int64_t x = (int64_t)j.m * j.ldx * 4, a = (int64_t)j.m * j.lda * 4;   // two parts of 2 bytes
-  j.sums = reinterpret_cast<double*>(take(kNormBlocks * 8));
+  j.sums = reinterpret_cast<double*>(take(kMaxParts * 8));
   j.x[0] = reinterpret_cast<_Float16*>(take(x));
   j.x[1] = reinterpret_cast<_Float16*>(take(x));
   j.A = reinterpret_cast<_Float16*>(take(a));
@@ -441,6 +586,8 @@ int64_t fill(Jobs& jobs, const NsJob* in, int count, unsigned char* ws) {
     j.n = (int)(j.tall ? s.R : s.C);
     j.lda = (int)up(j.m, 64);
     j.ldx = (int)up(j.n, 64);
+    const int64_t parts = ((int64_t)j.m * j.n + kNormChunk - 1) / kNormChunk;
+    j.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
     j.g32 = s.g32;
     j.out32 = s.out32;
     at += lay_out(j, ws ? ws + at : nullptr);
@@ -470,7 +617,7 @@ void step(Jobs& jobs, const NsParams& prm, int k, hipStream_t s) {
   });
   hipLaunchKernelGGL((ns_product_kernel<kGram, SPLIT, false>), dim3(square), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
   hipLaunchKernelGGL((ns_product_kernel<kPoly, SPLIT, false>), dim3(square), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
-  const unsigned wide = deal(jobs, [](const Job& j) { return up(j.m, kTile) / kTile * (up(j.n, kTile) / kTile); });
+  const unsigned wide = deal(jobs, [](const Job& j) { return up(up(j.m, kTile) / kTile * (up(j.n, kTile) / kTile), 8); });
   if (k + 1 < prm.steps)
     hipLaunchKernelGGL((ns_product_kernel<kApply, SPLIT, false>), dim3(wide), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
   else
@@ -488,7 +635,7 @@ hipError_t launch_newton_schulz(const NsJob* in, int count, const NsParams& prm,
   Jobs jobs{};
   fill(jobs, in, count, static_cast<unsigned char*>(ws));
   if (jobs.count == 0) return hipSuccess;
-  const unsigned norm = deal(jobs, [](const Job&) { return (int64_t)kNormBlocks; });
+  const unsigned norm = deal(jobs, [](const Job& j) { return (int64_t)j.parts; });
   hipLaunchKernelGGL(ns_norm_kernel, dim3(norm), dim3(kThreads), 0, s, jobs, prm.mu, prm.nesterov);
   const unsigned start = deal(jobs, [](const Job& j) { return up(j.m, 64) / 64 * (int64_t)(j.ldx / 64); });
   hipLaunchKernelGGL(ns_start_kernel, dim3(start), dim3(kThreads), 0, s, jobs, prm.mu, prm.nesterov, prm.eps);
