@@ -495,7 +495,7 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  *                    pointers in jobs do not matter to it)
  * Errors: NULL, SHAPE (also count or steps out of range), ALIGN, LAUNCH;
  * UNSUPPORTED for another type or a negative eps; WORKSPACE; TOO_LARGE when a
- * job's (min(R, C) + 128) * (max(R, C) + 128) reaches 2^30.
+ * job's (min(R, C) + 128) * (max(R, C) + 128) reaches 2^29.
  */
 typedef struct sp24_ortho_job {
   const void* G;

@@ -105,8 +105,8 @@ int check_embed_bwd(int64_t T, int64_t V, int64_t d) {
 int check_ns_shape(int64_t R, int64_t C) {
   const int st = check_dims(R, C, 1);
   if (st != SP24_OK) return st;
-  // rows of tiles past the matrix's end still have 32-bit byte offsets
-  return R != 0 && C != 0 && R + 128 >= ((int64_t)1 << 30) / (C + 128) ? SP24_ERR_TOO_LARGE : SP24_OK;
+  // byte offsets into both parts of X stay below 2^31
+  return R != 0 && C != 0 && R + 128 >= ((int64_t)1 << 29) / (C + 128) ? SP24_ERR_TOO_LARGE : SP24_OK;
 }
 
 int ns_params(const float* coef, int steps, float eps, sp24::NsParams& prm) {

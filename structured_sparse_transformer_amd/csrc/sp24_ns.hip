@@ -17,13 +17,16 @@
 // up to 16 fit and the typical ones keep all 11 bits.  Beside the rounded
 // part hi, X keeps the rest lo = fp16(x - hi), 22 bits together.  Products are
 // accumulated in fp32 in either mode:
-//   rounded   products of the hi parts.  X's lo part still enters a X in the
-//             first kLoSteps steps: there the small singular values grow 3.4
-//             times a step, and with them the rounding error of X, which
-//             without the lo part costs up to 6e-3 of the result's norm on a
-//             low-rank update.  Results are within about 2e-3 of exact
-//             arithmetic (bf16 operands: 1e-2 to 5e-2).
+//   rounded   products of the hi parts.  The first kLoSteps steps take a X in
+//             the epilogue, from both parts: there the small singular values
+//             grow 3.4 times a step, and with them the rounding error of X,
+//             which costs up to 6e-3 of the result's norm on a low-rank update
+//             if neither step does so, and 1.5e-3 after two that do.  Results
+//             are within about 2e-3 of exact arithmetic (bf16 operands: 1e-2
+//             to 5e-2).
 //   split     hi hi + hi lo + lo hi, for results to fp32 accuracy.
+// All other steps have a I in B (Q = a I + B, X <- Q X), so that the last
+// product of a step reads X once and writes what the next one needs.
 //
 // A and B are symmetric: only tiles on and above the diagonal are computed,
 // each stored twice.
@@ -33,6 +36,8 @@
 //   D: column l % 32, rows 8*(i/4) + 4g + i%4 for accumulator i
 #include <hip/hip_runtime.h>
 #include <cstdint>
+#include <type_traits>
+#include <utility>
 
 #include "sp24_device.hpp"
 #include "sp24_internal.hpp"
@@ -50,10 +55,9 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 
 constexpr int kThreads = 256;
 constexpr float kScale = 4096.0f, kInvScale = 1.0f / 4096.0f;   // the units of X, A and B
-constexpr int kLoSteps = 3;
+constexpr int kLoSteps = 2;
 constexpr int kNormChunk = 16 * kThreads;   // entries a workgroup squares at a time
 constexpr int kMaxParts = 1024;             // partial sums of squares per weight
-constexpr int kTile = 128;         // square tiles of the products
 constexpr int kBK = 32;            // reduction per stage
 
 // One weight, as the kernels see it.
@@ -65,13 +69,15 @@ struct Job {
   uint16_t* W;
   float lr, keep;
   int m, n;        // short and long side
-  int lda, ldx;    // row lengths of A, B and of X, multiples of 64
+  int na, nx;      // blocks of 32 along them: A and B are na x na blocks, X na x nx
   bool tall;       // X is U^T
   bool g32, out32;
   double* sums;                  // of squares, `parts` of them
   int parts;
   _Float16* x[2];                // X, hi then lo part, before and after a step
   _Float16 *A, *B;               // hi then lo part
+  int gram_splits;               // items that share the reduction of a tile of A
+  float* partial;                // their sums
   int first;                     // first workgroup of the launch at hand
 };
 struct Jobs {
@@ -131,6 +137,15 @@ __device__ __forceinline__ float update_of(const Job& j, int64_t i, float mu, bo
   return nesterov ? load_g(j, i) + mu * m : m;
 }
 
+__device__ __forceinline__ void update8(const Job& j, int64_t i, float mu, bool nesterov, float (&u)[8]) {
+  load8(j.G, j.g32, i, i + 8, u);
+  if (j.M == nullptr) return;
+  float m[8];
+  load8(j.M, true, i, i + 8, m);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = nesterov ? u[e] + mu * m[e] : m[e];
+}
+
 // Sum over the workgroup, in every thread; a fixed order.
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double s[kThreads / 64];
@@ -178,58 +193,18 @@ __global__ __launch_bounds__(kThreads) void ns_norm_kernel(Jobs jobs, float mu, 
   if (threadIdx.x == 0) j.sums[block] = sum;
 }
 
+// X, A and B are stored in blocks of 32 x 32, row-major among themselves and
+// within: element (r, c) of a matrix of nb blocks a row.  A stage of a product
+// reads whole blocks (2 KiB), whichever side of the reduction its rows are on;
+// row-major matrices would give it half cache lines.
+__device__ __forceinline__ int64_t at_block(int r, int c, int nb) {
+  return ((int64_t)(r >> 5) * nb + (c >> 5)) * 1024 + (r & 31) * 32 + (c & 31);
+}
+
 // x in two fp16 parts
 __device__ __forceinline__ void split(float x, _Float16& hi, _Float16& lo) {
   hi = (_Float16)x;
   lo = (_Float16)(x - (float)hi);
-}
-
-// X_0 in both parts, a 64 x 64 tile of it a workgroup; the columns from n to
-// ldx are zeros.
-__global__ __launch_bounds__(kThreads) void ns_start_kernel(Jobs jobs, float mu, bool nesterov, float eps) {
-  __shared__ float tile[64][65];
-  const Job& j = job_of(jobs, blockIdx.x);
-  const int block = blockIdx.x - j.first, tiles_n = j.ldx / 64;
-  const int i0 = block / tiles_n * 64, j0 = block % tiles_n * 64;
-  double sum = 0.0;
-  for (int k = threadIdx.x; k < j.parts; k += kThreads) sum += j.sums[k];
-  const double norm = sqrt(block_sum(sum));
-  const double scale = (double)kScale / (norm + (double)eps);
-  const int64_t plane = (int64_t)j.m * j.ldx;
-  if (j.tall) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int k = e * kThreads + threadIdx.x, r = j0 + k / 64, c = i0 + k % 64;   // of U [n][m]
-      tile[k / 64][k % 64] = r < j.n && c < j.m ? update_of(j, (int64_t)r * j.m + c, mu, nesterov) : 0.0f;
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int k = e * kThreads + threadIdx.x, r = i0 + k / 64, c = j0 + k % 64;
-    if (r >= j.m) continue;
-    float u;
-    if (j.tall)
-      u = tile[k % 64][k / 64];
-    else
-      u = c < j.n ? update_of(j, (int64_t)r * j.n + c, mu, nesterov) : 0.0f;
-    _Float16 hi, lo;
-    split((float)((double)u * scale), hi, lo);
-    j.x[0][(int64_t)r * j.ldx + c] = hi;
-    j.x[0][plane + (int64_t)r * j.ldx + c] = lo;
-  }
-}
-
-// vmcnt wait (expcnt and lgkmcnt not waited for)
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-// What one lane of a wave has written to LDS is read by the others.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // Eight values in their fp16 parts; 16-byte aligned.
@@ -246,308 +221,565 @@ __device__ __forceinline__ void put8(_Float16* p, int64_t plane, bool both, cons
   if (both) *reinterpret_cast<h8*>(p + plane) = lo;
 }
 
-// Entries at .. at + 7 of a result's row of n, which starts at entry `row`:
-// the orthogonalised update, or the weight's step by it.
-__device__ __forceinline__ void finish8(const Job& j, int64_t row, int at, int n, const float (&v)[8]) {
-  const bool whole = at + 8 <= n && n % 8 == 0;   // rows start 16-byte aligned
-  const int64_t o = row + at;
-  if (j.P != nullptr) {
-    float p[8];
-    if (whole) {
-      load8(j.P, true, o, o + 8, p);
+// X_0 in both parts, 32 x 64 of it a workgroup (two blocks side by side);
+// zeros past m and n.
+__global__ __launch_bounds__(kThreads) void ns_start_kernel(Jobs jobs, float mu, bool nesterov, float eps) {
+  __shared__ float tile[64][33];
+  const Job& j = job_of(jobs, blockIdx.x);
+  const int block = blockIdx.x - j.first, tiles_n = (j.nx + 1) / 2;
+  const int i0 = block / tiles_n * 32, j0 = block % tiles_n * 64;
+  const int tid = threadIdx.x;
+  // this thread's eight entries of a row of X
+  const int r = tid >> 3, c = (tid & 7) * 8;
+  float u[8];
+  if (!j.tall) {
+    // of a row of U
+    const int row = i0 + r, col = j0 + c;
+    const int64_t i = (int64_t)row * j.n + col;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = j.keep * p[e] - j.lr * v[e];
-      store8(j.P, o, o + 8, p);
-      if (j.W != nullptr) {
-        h8 h;
+    for (int e = 0; e < 8; ++e) u[e] = 0.0f;
+    if (row < j.m) {
+      if (j.n % 8 == 0) {
+        if (col < j.n) update8(j, i, mu, nesterov, u);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = (_Float16)p[e];
-        *reinterpret_cast<h8*>(j.W + o) = h;
+        for (int e = 0; e < 8; ++e)
+          if (col + e < j.n) u[e] = update_of(j, i + e, mu, nesterov);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = at + e < n ? j.P[o + e] : 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (at + e >= n) continue;
-        p[e] = j.keep * p[e] - j.lr * v[e];
-        j.P[o + e] = p[e];
-        if (j.W != nullptr) j.W[o + e] = __builtin_bit_cast(uint16_t, (_Float16)p[e]);
-      }
-    }
-    return;
-  }
-  if (j.out32) {
-    float* out = static_cast<float*>(j.out);
-    if (whole) {
-      store8(out, o, o + 8, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e < n) out[o + e] = v[e];
     }
   } else {
-    _Float16* out = static_cast<_Float16*>(j.out);
-    if (whole) {
-      h8 h;
+    // U [n][m]: 64 rows of 32, turned in LDS
+    const int row = j0 + (tid >> 2), col = i0 + (tid & 3) * 8;
+    const int64_t i = (int64_t)row * j.m + col;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
-      *reinterpret_cast<h8*>(out + o) = h;
-    } else {
+    for (int e = 0; e < 8; ++e) u[e] = 0.0f;
+    if (row < j.n) {
+      if (j.m % 8 == 0) {
+        if (col < j.m) update8(j, i, mu, nesterov, u);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e < n) out[o + e] = (_Float16)v[e];
+        for (int e = 0; e < 8; ++e)
+          if (col + e < j.m) u[e] = update_of(j, i + e, mu, nesterov);
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[tid >> 2][(tid & 3) * 8 + e] = u[e];
   }
+  double sum = 0.0;
+  for (int k = tid; k < j.parts; k += kThreads) sum += j.sums[k];
+  const double norm = sqrt(block_sum(sum));   // its barrier also orders the turn
+  const double scale = (double)kScale / (norm + (double)eps);
+  if (j.tall) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = tile[c + e][r];
+  }
+  if ((j0 >> 5) + (c >> 5) >= j.nx) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) u[e] = (float)((double)u[e] * scale);
+  put8(j.x[0] + at_block(i0 + r, j0 + c, j.nx), (int64_t)j.na * j.nx * 1024, true, u);
+}
+
+// vmcnt wait (expcnt and lgkmcnt not waited for)
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// What one lane of a wave has written to LDS is read by the others.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 enum : int { kGram = 0, kPoly = 1, kApply = 2 };
 
-// The products' LDS stage: kTile rows x kBK of the left operand, then the
-// right operand: kTile rows x kBK (kGram, kPoly: both are rows along the
-// reduction), or kBK rows x kTile columns of X (kApply).  Rows of kBK halves
-// are four 16-byte chunks; chunk c of row r is stored at c ^ (r / 4 % 4), so
-// that the 16 rows a fragment read serves at a time cover all banks once.
-// Rows of kTile columns are read by transpose reads; their chunk q is at
-// (q + 12 (r % 4)) % 16, which puts the eight 32-byte windows that a read
-// fetches from four rows in different banks.
-constexpr int kOperand = kTile * kBK * 2;   // bytes of one operand's part
-constexpr int kRing = 3;
-constexpr int kTurn = 68;   // floats in a row of the epilogue's 32 x 64 blocks
-static_assert(4 * 32 * kTurn * 4 <= kRing * 2 * kOperand, "the epilogue's blocks fit the ring");
+// A product's tile: BM x BN a workgroup, WM x WN each of its waves; RING stages
+// of its operands in LDS, and at least OCC waves on a SIMD.
+template <int BM_, int BN_, int WM_, int WN_, int RING_, int OCC_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, RING = RING_, OCC = OCC_;
+  static constexpr int WAVES_M = BM / WM, WAVES = WAVES_M * (BN / WN), TM = WM / 32, TN = WN / 32;
+  static_assert(TN % 2 == 0, "columns in pairs of blocks");
+};
 
-template <int KIND, bool SPLIT, bool LAST>
-__global__ __launch_bounds__(kThreads) void ns_product_kernel(Jobs jobs, int cur, float a, float b, float c, bool use_lo) {
+
+// The products' LDS stage: the BM / 32 blocks of the left operand's parts, then
+// the BN / 32 of the right one's, each 32 rows of four 16-byte chunks.  Rows run
+// along the reduction, but those of kApply's right operand, X, across it: its
+// fragments are made by transpose reads.  Chunk c of row r is stored at
+// c ^ (r / 4 % 4): the 16 rows that a plain read serves at a time then cover all
+// banks once, and the four rows of a transpose read are whole rows either way.
+
+// Floats in a row of the epilogue's blocks of 32 x 64, one a wave.
+constexpr int kTurn = 68;
+
+// dma_b128 with a part of the offset in a scalar register.
+__device__ __forceinline__ void dma_at(i32x4 rsrc, uint32_t lds, uint32_t voffset, int soffset) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(voffset), "s"(rsrc), "s"(soffset), "{m0}"(lds)
+               : "memory");
+}
+
+// The tiles of A and B: those on and above the diagonal, row by row.  Tiles are
+// as high as wide or a whole part of that, and the ones that hold the diagonal
+// cover its whole squares; the others are mirrored.
+template <class T>
+__host__ __device__ __forceinline__ int64_t upper_tiles(int m) {
+  constexpr int Q = T::BN / T::BM;
+  static_assert(T::BN % T::BM == 0, "diagonal squares");
+  const int64_t rows = (m + T::BM - 1) / T::BM, cols = (m + T::BN - 1) / T::BN, full = rows / Q, rest = rows % Q;
+  return rows * cols - Q * (full * (full - 1) / 2) - rest * full;   // row r holds cols - r / Q
+}
+template <class T>
+__device__ __forceinline__ void upper_tile(int m, int k, int& tm, int& tn) {
+  constexpr int Q = T::BN / T::BM;
+  const int cols = (m + T::BN - 1) / T::BN;
+  tm = 0;
+  while (k >= cols - tm / Q) k -= cols - tm++ / Q;
+  tn = tm / Q + k;
+}
+
+// What a step's kernels take besides the weights.
+struct Step {
+  int cur;          // which of x[] holds X
+  float a, b, c;
+  bool in_q;        // a I is in B
+  bool write_lo;    // the next step needs X's lo part
+};
+
+// The end of a product for 32 rows from r0 and 64 columns from c0 of its result,
+// in a wave's accumulators v0 and v1 (32 columns each): A; B = b A + c v, with
+// a I or without; X <- a X + v (ADD) or v; or the outcome of the last step.  They are turned through the
+// wave's block of LDS, so that a lane holds 8 columns of a row and what it reads
+// and writes is whole 16-byte pieces of contiguous runs.  What goes out
+// transposed (the mirrored tile, a tall weight) is put back and read by columns.
+template <int KIND, bool SPLIT, bool LAST, bool ADD>
+__device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror, int r0, int c0, const f16v& v0,
+                                       const f16v& v1, float* turn, int lane) {
+  const int g = lane >> 5, l32 = lane & 31, er = lane >> 3, ec = (lane & 7) * 8;
+  // what is read, and what is written: X, or A and B, of one shape
+  const _Float16* const old = KIND == kApply ? j.x[st.cur] : j.A;
+  _Float16* const D = KIND == kGram ? j.A : KIND == kPoly ? j.B : j.x[1 - st.cur];
+  const int nb = KIND == kApply ? j.nx : j.na;
+  const int64_t plane = (int64_t)j.na * nb * 1024;
+  const bool in = r0 < 32 * j.na && c0 + ec < 32 * nb;
+  const int64_t at0 = at_block(r0 + er, c0 + ec, nb);   // rows 8 apart are 256 elements apart
+  constexpr bool kLoads = KIND == kPoly || ADD;
+  h8 ohi[4], olo[4];
+  if constexpr (kLoads) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      ohi[p] = olo[p] = h8{};
+      if (in) {
+        ohi[p] = *reinterpret_cast<const h8*>(old + at0 + p * 256);
+        if constexpr (SPLIT || ADD) olo[p] = *reinterpret_cast<const h8*>(old + at0 + p * 256 + plane);
+      }
+    }
+  }
+  // the outcome's place: rows of n, or for a tall weight of m, read and written
+  // 16 bytes at a time where they allow it
+  const bool by_col = KIND == kApply ? LAST && j.tall : mirror;
+  const int width = j.tall ? j.m : j.n;
+  const bool whole = width % 8 == 0;
+  int64_t o[4];
+  int left[4];   // entries of the eight that exist
+  float pw[4][8];
+  if constexpr (LAST) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int row = j.tall ? c0 + p * 16 + (lane >> 2) : r0 + p * 8 + er;
+      const int col = j.tall ? r0 + (lane & 3) * 8 : c0 + ec;
+      o[p] = (int64_t)row * width + col;
+      left[p] = row < (j.tall ? j.n : j.m) ? min(8, width - col) : 0;
+      if (whole && j.P != nullptr && left[p] > 0) load8(j.P, true, o[p], o[p] + 8, pw[p]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float* const to = turn + (8 * (i >> 2) + 4 * g + (i & 3)) * kTurn + l32;
+    to[0] = v0[i];
+    to[32] = v1[i];
+  }
+  wave_sync();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float* const mine = turn + (p * 8 + er) * kTurn + ec;
+    const f4 x = *reinterpret_cast<const f4*>(mine), y = *reinterpret_cast<const f4*>(mine + 4);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = (e < 4 ? x[e & 3] : y[e & 3]) * kInvScale;
+      if constexpr (kLoads) {
+        const float was = (float)ohi[p][e] + (float)olo[p][e];
+        v[e] = KIND == kPoly ? st.b * was + st.c * v[e] : st.a * was + v[e];
+        if constexpr (KIND == kPoly)
+          if (st.in_q && r0 + p * 8 + er == c0 + ec + e) v[e] += st.a * kScale;
+      }
+      if constexpr (LAST) v[e] *= kInvScale;
+    }
+    if constexpr (!LAST)
+      if (in) put8(D + at0 + p * 256, plane, SPLIT || (KIND == kApply && st.write_lo), v);
+    if (LAST || by_col) {
+      *reinterpret_cast<f4*>(mine) = f4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f4*>(mine + 4) = f4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  if (LAST || by_col) {
+    wave_sync();
+    const int step = by_col ? kTurn : 1;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float* const from = by_col ? turn + (lane & 3) * 8 * kTurn + p * 16 + (lane >> 2) : turn + (p * 8 + er) * kTurn + ec;
+      if constexpr (!LAST) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = from[e * step];
+        const int row = c0 + p * 16 + (lane >> 2), col = r0 + (lane & 3) * 8;
+        if (row < 32 * j.na && col < 32 * j.na) put8(D + at_block(row, col, nb), plane, SPLIT, v);
+      } else if (whole) {
+        if (left[p] <= 0) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = from[e * step];
+        if (j.P != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = j.keep * pw[p][e] - j.lr * v[e];
+          store8(j.P, o[p], o[p] + 8, v);
+        }
+        if (j.P == nullptr && j.out32) {
+          store8(static_cast<float*>(j.out), o[p], o[p] + 8, v);
+        } else if (j.P == nullptr || j.W != nullptr) {
+          h8 h;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
+          *reinterpret_cast<h8*>((j.P != nullptr ? reinterpret_cast<_Float16*>(j.W) : static_cast<_Float16*>(j.out)) + o[p]) = h;
+        }
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < left[p]; ++e) {
+          float v = from[e * step];
+          const int64_t i = o[p] + e;
+          if (j.P != nullptr) {
+            v = j.keep * j.P[i] - j.lr * v;
+            j.P[i] = v;
+            if (j.W != nullptr) j.W[i] = __builtin_bit_cast(uint16_t, (_Float16)v);
+          } else if (j.out32) {
+            static_cast<float*>(j.out)[i] = v;
+          } else {
+            static_cast<_Float16*>(j.out)[i] = (_Float16)v;
+          }
+        }
+      }
+    }
+  }
+  wave_sync();   // the block has been read
+}
+
+template <int KIND, bool SPLIT, bool LAST, bool ADD, class T>
+__global__ __launch_bounds__(64 * T::WAVES, T::OCC) void ns_product_kernel(Jobs jobs, Step st) {
   constexpr int PARTS = SPLIT ? 2 : 1;
-  constexpr int STAGE = 2 * PARTS * kOperand;
-  constexpr int LOADS = kOperand / 1024 / 4;   // direct loads per wave, operand and part
-  __shared__ __align__(1024) unsigned char smem[kRing * STAGE];
+  constexpr int LEFT = T::BM * kBK * 2, RIGHT = T::BN * kBK * 2;   // bytes of one operand's part
+  constexpr int STAGE = PARTS * (LEFT + RIGHT);
+  constexpr int LL = LEFT / 1024, RL = RIGHT / 1024;   // 1 KiB direct loads of a part
+  constexpr int W = T::WAVES, LN = (PARTS * LL + W - 1) / W, RN = (PARTS * RL + W - 1) / W;   // a wave's, at most
+  static_assert((T::RING - 2) * (LN + RN) < 64, "vmcnt immediate");
+  static_assert(W * 32 * kTurn * 4 <= T::RING * STAGE, "the epilogue's blocks fit the ring");
+  __shared__ __align__(1024) unsigned char smem[T::RING * STAGE];
   const Job& j = job_of(jobs, blockIdx.x);
-  int block = blockIdx.x - j.first;
-  const int tiles_m = (j.m + kTile - 1) / kTile;
+  const int block = blockIdx.x - j.first;
+  const int tiles_m = (j.m + T::BM - 1) / T::BM;
+
+  // Workgroups go round the 8 XCDs; each takes a run of the items, so that its
+  // L2 fetches an operand strip or a slice of the reduction once.
+  int tiles;
+  if constexpr (KIND == kApply)
+    tiles = tiles_m * ((j.n + T::BN - 1) / T::BN);
+  else
+    tiles = (int)upper_tiles<T>(j.m);
+  const int splits = KIND == kGram ? j.gram_splits : 1;
+  const int items = tiles * splits, run = (items + 7) / 8;
+  const int lin = block % 8 * run + block / 8;
+  if (block / 8 >= run || lin >= items) return;
+  const int tile = lin % tiles, sp = lin / tiles;
   int tm, tn;
   if constexpr (KIND == kApply) {
-    // workgroups go round the 8 XCDs: each takes a run of column strips, whose
-    // X its L2 then fetches once
-    const int tiles = tiles_m * ((j.n + kTile - 1) / kTile), run = (tiles + 7) / 8;
-    const int lin = block % 8 * run + block / 8;
-    if (block / 8 >= run || lin >= tiles) return;
-    tm = lin % tiles_m;
-    tn = lin / tiles_m;
+    tm = tile % tiles_m;
+    tn = tile / tiles_m;
   } else {
-    // row tm of the upper triangle holds tiles_m - tm tiles
-    tm = 0;
-    while (block >= tiles_m - tm) block -= tiles_m - tm++;
-    tn = tm + block;
+    upper_tile<T>(j.m, tile, tm, tn);
   }
   tm = __builtin_amdgcn_readfirstlane(tm);
   tn = __builtin_amdgcn_readfirstlane(tn);
-  const int m0 = tm * kTile, n0 = tn * kTile;
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % T::WAVES_M, wn = wave / T::WAVES_M;
   const int g = lane >> 5, l32 = lane & 31;
 
-  const int64_t xplane = (int64_t)j.m * j.ldx, aplane = (int64_t)j.m * j.lda;
-  const _Float16* const X = j.x[cur];
+  const int64_t xplane = (int64_t)j.na * j.nx * 1024, aplane = (int64_t)j.na * j.na * 1024;
+  const _Float16* const X = j.x[st.cur];
   const _Float16* const left = KIND == kGram ? X : KIND == kPoly ? j.A : j.B;
   const _Float16* const right = KIND == kPoly ? j.A : X;
-  const int lld = KIND == kGram ? j.ldx : j.lda, rld = KIND == kPoly ? j.lda : j.ldx;
+  const int lnb = KIND == kGram ? j.nx : j.na, rnb = KIND == kPoly ? j.na : j.nx;
   const int64_t lplane = KIND == kGram ? xplane : aplane, rplane = KIND == kPoly ? aplane : xplane;
-  const int nk = lld / kBK;
+  // this item's stages of the reduction
+  const int nk_all = lnb, k_lo = nk_all * sp / splits, nk = nk_all * (sp + 1) / splits - k_lo;
 
-  // Descriptors over whole parts: rows past m read as zero.  Columns of X past
-  // ldx are the next row's and feed only outputs that are not stored.
-  i32x4 rl[PARTS], rr[PARTS];
+  // One descriptor over each operand's parts.  This wave's direct loads of a
+  // stage are every W-th KiB of the left operand's, then of the right one's;
+  // a lane's offset is that of the chunk that belongs in its slot, and past
+  // everything, which reads as zero, for blocks outside the matrix.
+  const i32x4 lrsrc = make_rsrc(left, (uint32_t)(PARTS * lplane * 2)), rrsrc = make_rsrc(right, (uint32_t)(PARTS * rplane * 2));
+  constexpr int kBlock = 2048;
+  constexpr uint32_t kNowhere = 0x80000000u;
+  const int left_step = kBlock, right_step = KIND == kApply ? rnb * kBlock : kBlock;
+  uint32_t loff[LN], roff[RN];
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p) {
-    rl[p] = make_rsrc(left + p * lplane, (uint32_t)(lplane * 2));
-    rr[p] = make_rsrc(right + p * rplane, (uint32_t)(rplane * 2));
+  for (int u = 0; u < LN; ++u) {
+    const int ld = wave + W * u, s = ld % LL * 64 + lane, row = s / 4 % 32, blk = m0 / 32 + s / 128;
+    loff[u] = blk < j.na ? (uint32_t)(ld / LL * lplane * 2 + ((int64_t)blk * lnb + k_lo) * kBlock + row * 64 + ((s & 3) ^ (row >> 2 & 3)) * 16)
+                         : kNowhere;
   }
-  int goff_l[LOADS], goff_r[LOADS];
 #pragma unroll
-  for (int u = 0; u < LOADS; ++u) {
-    const int s = (wave + 4 * u) * 64 + lane;   // 16-byte slot of the operand's part
-    {
-      const int row = s / 4, q = (s & 3) ^ ((row >> 2) & 3);
-      goff_l[u] = (m0 + row) * lld * 2 + q * 16;
-      if constexpr (KIND != kApply) goff_r[u] = (n0 + row) * rld * 2 + q * 16;
-    }
-    if constexpr (KIND == kApply) {
-      const int row = s / 16, q = ((s & 15) + 16 - 12 * (row & 3) % 16) & 15;
-      goff_r[u] = row * rld * 2 + (n0 + 8 * q) * 2;
-    }
+  for (int u = 0; u < RN; ++u) {
+    const int ld = wave + W * u, s = ld % RL * 64 + lane, row = s / 4 % 32, blk = n0 / 32 + s / 128;
+    const int64_t first = KIND == kApply ? (int64_t)k_lo * rnb + blk : (int64_t)blk * rnb + k_lo;
+    roff[u] = blk < (KIND == kApply ? rnb : j.na)
+                  ? (uint32_t)(ld / RL * rplane * 2 + first * kBlock + row * 64 + ((s & 3) ^ (row >> 2 & 3)) * 16)
+                  : kNowhere;
   }
-  const int right_step = KIND == kApply ? kBK * rld * 2 : kBK * 2;
-  auto issue = [&](int kt, int slot) {
+  const uint32_t ring = lds_addr(smem) + 1024 * wave;
+  auto issue_one = [&](int u, int kt, int slot) __attribute__((always_inline)) {
+    const uint32_t dst = ring + slot * STAGE;
+    if (u < LN) {
+      if (W * (u + 1) <= PARTS * LL || wave < PARTS * LL % W) dma_at(lrsrc, dst + 1024 * W * u, loff[u], kt * left_step);
+    } else {
+      const int v = u - LN;
+      if (W * (v + 1) <= PARTS * RL || wave < PARTS * RL % W)
+        dma_at(rrsrc, dst + PARTS * LEFT + 1024 * W * v, roff[v], kt * right_step);
+    }
+  };
+  auto issue = [&](int kt, int slot) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-      for (int u = 0; u < LOADS; ++u) {
-        const uint32_t dst = lds_addr(smem) + slot * STAGE + p * kOperand + 1024 * (wave + 4 * u);
-        dma_b128(rl[p], dst, goff_l[u] + kt * kBK * 2);
-        dma_b128(rr[p], dst + PARTS * kOperand, goff_r[u] + kt * right_step);
-      }
+    for (int u = 0; u < LN + RN; ++u) issue_one(u, kt, slot);
+  };
+  // allow `stages` stages of this wave's loads to stay in flight
+  const int nl = PARTS * LL / W + PARTS * RL / W + (wave < PARTS * LL % W) + (wave < PARTS * RL % W);
+  auto wait_loads = [&]<int I>(std::integral_constant<int, I>) __attribute__((always_inline)) {
+    constexpr int lo = PARTS * LL / W + PARTS * RL / W;
+    if (PARTS * LL % W == 0 && PARTS * RL % W == 0)
+      wait_vm<I * lo>();
+    else if (nl == lo)
+      wait_vm<I * lo>();
+    else if (nl == lo + 1)
+      wait_vm<I * (lo + 1)>();
+    else
+      wait_vm<I * (lo + 2)>();
   };
 
-  // this lane's fragment offsets inside an operand's part, per 32-row block
-  int l_off[2], r_off[2];
+  // this lane's fragment offsets inside an operand's part, per block
+  int l_off[T::TM], r_off[T::TN];
+  const int G = lane >> 4, j4 = (lane & 15) >> 2, c4 = lane & 3;   // transpose reads: 16-lane group, row, 4 columns
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int row = wm * 64 + t * 32 + l32;
-    l_off[t] = row * 64;
-    if constexpr (KIND != kApply) {
-      r_off[t] = (wn * 64 + t * 32 + l32) * 64;
-    } else {
-      const int G = lane >> 4, j4 = (lane & 15) >> 2, c4 = lane & 3;
-      const int q = (wn * 64 + t * 32 + 16 * (G & 1)) / 8 + (c4 >> 1);
-      r_off[t] = (8 * (G >> 1) + j4) * 256 + ((q + 12 * j4) & 15) * 16 + (c4 & 1) * 8;
-    }
-  }
-  const int swz = (l32 >> 2) & 3;   // of both operands' rows: their blocks start at multiples of 32
+  for (int t = 0; t < T::TM; ++t) l_off[t] = (wm * T::TM + t) * kBlock + l32 * 64;
+#pragma unroll
+  for (int t = 0; t < T::TN; ++t)
+    r_off[t] = PARTS * LEFT + (wn * T::TN + t) * kBlock + (KIND == kApply ? (8 * (G >> 1) + j4) * 64 + (c4 & 1) * 8 : l32 * 64);
+  const int swz = (l32 >> 2) & 3;
   auto row_frag = [&](int base, int ks) -> h8 {
     return *reinterpret_cast<const h8*>(smem + base + (((2 * ks + g) ^ swz) * 16));
   };
+  // rows 8 (G / 2) + j4 and the row 4 below, columns 16 (G % 2) + 4 c4 .. + 3
+  const int tr_q = 2 * (G & 1) + (c4 >> 1), tr_lo = (tr_q ^ (2 * (G >> 1))) * 16, tr_hi = (tr_q ^ (2 * (G >> 1) + 1)) * 16 + 4 * 64;
   auto tr_frag = [&](int base, int ks) -> h8 {
-    const int o = base + ks * 16 * 256;
-    const h4 lo = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)((lds_u8*)smem + o)));
-    const h4 hi = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)((lds_u8*)smem + o + 4 * 256)));
+    const int o = base + ks * 16 * 64;
+    const h4 lo = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)((lds_u8*)smem + o + tr_lo)));
+    const h4 hi = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)((lds_u8*)smem + o + tr_hi)));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
+  struct Frags {
+    h8 l[PARTS][T::TM], r[PARTS][T::TN];
+  };
+  // fragments of step ks (of 16) of the stage in ring slot `slot`
+  auto load_frags = [&](int slot, int ks, Frags& f) __attribute__((always_inline)) {
+    const int base = slot * STAGE;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+#pragma unroll
+      for (int t = 0; t < T::TM; ++t) f.l[p][t] = row_frag(base + p * LEFT + l_off[t], ks);
+#pragma unroll
+      for (int t = 0; t < T::TN; ++t) {
+        if constexpr (KIND == kApply)
+          f.r[p][t] = tr_frag(base + p * RIGHT + r_off[t], ks);
+        else
+          f.r[p][t] = row_frag(base + p * RIGHT + r_off[t], ks);
+      }
+    }
+  };
 
-  f16v acc[2][2];
+  f16v acc[T::TM][T::TN];
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+  for (int s = 0; s < T::TM; ++s)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < T::TN; ++t)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[s][t][e] = 0.0f;
+  // the MFMAs of one step; with LOAD this wave's loads of stage kt go out
+  // between them
+  auto mfmas = [&]<bool LOAD>(const Frags& f, std::bool_constant<LOAD>, int kt, int slot) __attribute__((always_inline)) {
+    constexpr int each = (LN + RN + T::TM * T::TN - 1) / (T::TM * T::TN);
+#pragma unroll
+    for (int s = 0; s < T::TM; ++s)
+#pragma unroll
+      for (int t = 0; t < T::TN; ++t) {
+        if constexpr (SPLIT) {
+          acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.l[0][s], f.r[1][t], acc[s][t], 0, 0, 0);
+          acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.l[1][s], f.r[0][t], acc[s][t], 0, 0, 0);
+        }
+        acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.l[0][s], f.r[0][t], acc[s][t], 0, 0, 0);
+        if constexpr (LOAD) {
+#pragma unroll
+          for (int u = (s * T::TN + t) * each; u < (s * T::TN + t + 1) * each; ++u)
+            if (u < LN + RN) issue_one(u, kt, slot);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
 
-  constexpr int PER_STAGE = 2 * PARTS * LOADS;   // this wave's loads
-  issue(0, 0);
-  if (nk > 1) issue(1, 1);
-  for (int kt = 0; kt < nk; ++kt) {
-    // this wave's loads of stage kt are done, then every wave's; nobody reads
-    // the slot of stage kt - 1 any more, which stage kt + 2 takes
-    if (kt + 1 < nk) wait_vm<PER_STAGE>(); else wait_vm<0>();
-    __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));
+  // Pipeline: stage s goes to ring slot s % RING, RING stages ahead.  In a
+  // stage the second step's fragments are read during the first step's MFMAs;
+  // in its middle the wave waits for the next stage's loads and for its own
+  // reads, all waves meet (nobody reads this stage's slot afterwards), and the
+  // stage RING further is loaded into it while the next stage's first fragments
+  // are read.
+  constexpr int R = T::RING;
+#pragma unroll
+  for (int s = 0; s < R; ++s)
+    if (s < nk) issue(s, s);
+  if (nk > 0) {
+    // stages that may still be on their way when `left` of them come after the
+    // one that is needed
+    auto wait_at_most = [&](int left) __attribute__((always_inline)) {
+      [&]<int... I>(std::integer_sequence<int, I...>) __attribute__((always_inline)) {
+        ((left == I || (I == R - 1 && left > I) ? wait_loads(std::integral_constant<int, I>{}) : (void)0), ...);
+      }(std::make_integer_sequence<int, R>{});
+    };
+    wait_at_most(nk - 1);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kt + 2 < nk) issue(kt + 2, (kt + 2) % kRing);
-    const int base = (kt % kRing) * STAGE;
-#pragma unroll
-    for (int ks = 0; ks < kBK / 16; ++ks) {
-      h8 fl[PARTS][2], fr[PARTS][2];
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          fl[p][t] = row_frag(base + p * kOperand + l_off[t], ks);
-          const int rb = base + (PARTS + p) * kOperand + r_off[t];
-          if constexpr (KIND == kApply)
-            fr[p][t] = tr_frag(rb, ks);
-          else
-            fr[p][t] = row_frag(rb, ks);
-        }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if constexpr (SPLIT) {
-            acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[0][s], fr[1][t], acc[s][t], 0, 0, 0);
-            acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[1][s], fr[0][t], acc[s][t], 0, 0, 0);
-          }
-          acc[s][t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fl[0][s], fr[0][t], acc[s][t], 0, 0, 0);
-        }
-    }
-    asm volatile("" ::: "memory");
+    Frags f0, f1;
+    load_frags(0, 0, f0);
+    int slot = 0;
+    auto stage = [&]<bool LOAD>(std::bool_constant<LOAD>, int kt) __attribute__((always_inline)) {
+      const int next = slot + 1 == R ? 0 : slot + 1;
+      load_frags(slot, 1, f1);
+      __builtin_amdgcn_sched_barrier(0);
+      mfmas(f0, std::false_type{}, 0, 0);
+      if constexpr (LOAD)
+        wait_loads(std::integral_constant<int, R - 2>{});
+      else
+        wait_at_most(max(nk - 2 - kt, 0));
+      __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      load_frags(next, 0, f0);   // after the last stage: of no use, and none made
+      __builtin_amdgcn_sched_barrier(0);
+      mfmas(f1, std::bool_constant<LOAD>{}, kt + R, slot);
+      slot = next;
+    };
+    int kt = 0;
+#pragma unroll 1
+    for (; kt + R < nk; ++kt) stage(std::true_type{}, kt);
+#pragma unroll 1
+    for (; kt < nk; ++kt) stage(std::false_type{}, kt);
   }
-
-  // Epilogue.  A wave turns 32 rows x 64 columns of accumulators at a time
-  // through its quarter of the ring, so that a lane holds 8 columns of a row:
-  // what it reads and writes there is whole 16-byte pieces of 128-byte runs.
-  // Results that go out transposed (the mirrored tile, a tall weight) are put
-  // back and read again by columns.  The loads of a block are issued before
-  // its first store.
   __syncthreads();   // the ring is idle
-  float* const turn = reinterpret_cast<float*>(smem) + wave * (32 * kTurn);
-  const int er = lane >> 3, ec = (lane & 7) * 8;   // row (of 8) and first column
-  constexpr bool kLoads = KIND != kGram;
-  const bool back = KIND == kApply ? LAST && j.tall : tm != tn;
-  // what is read, and what is written: X, or A and B, of one shape
-  const _Float16* const old = KIND == kApply ? X : j.A;
-  _Float16* const D = KIND == kGram ? j.A : KIND == kPoly ? j.B : j.x[1 - cur];
-  const int64_t plane = KIND == kApply ? xplane : aplane;
-  const int ld = KIND == kApply ? j.ldx : j.lda;
-  const bool old_lo = SPLIT || (KIND == kApply && use_lo);
-  const int c0 = n0 + wn * 64 + ec;
-  const bool col_in = c0 < ld;
+
+  if constexpr (KIND == kGram) {
+    if (splits > 1) {
+      // the item's share of the sums, for ns_join_kernel
+      constexpr int FLOATS = T::BM * T::BN;
+      float* const mine = j.partial + ((int64_t)tile * splits + sp) * FLOATS + wave * (FLOATS / W);
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int r0 = m0 + wm * 64 + s * 32;
-    h8 ohi[4], olo[4];
-    if constexpr (kLoads) {
+      for (int s = 0; s < T::TM; ++s)
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int row = r0 + p * 8 + er;
-        ohi[p] = olo[p] = h8{};
-        if (row < j.m && col_in) {
-          const _Float16* at = old + (int64_t)row * ld + c0;
-          ohi[p] = *reinterpret_cast<const h8*>(at);
-          if (old_lo) olo[p] = *reinterpret_cast<const h8*>(at + plane);
-        }
-      }
+        for (int t = 0; t < T::TN; ++t)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f4*>(mine + ((s * T::TN + t) * 4 + q) * 256 + lane * 4) =
+                f4{acc[s][t][4 * q], acc[s][t][4 * q + 1], acc[s][t][4 * q + 2], acc[s][t][4 * q + 3]};
+      return;
     }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) turn[(8 * (i >> 2) + 4 * g + (i & 3)) * kTurn + t * 32 + l32] = acc[s][t][i];
-    wave_sync();
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int row = r0 + p * 8 + er;
-      float* const mine = turn + (p * 8 + er) * kTurn + ec;
-      const f4 v0 = *reinterpret_cast<const f4*>(mine), v1 = *reinterpret_cast<const f4*>(mine + 4);
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = (e < 4 ? v0[e & 3] : v1[e & 3]) * kInvScale;
-        if constexpr (kLoads) {
-          const float o = (float)ohi[p][e] + (float)olo[p][e];
-          v[e] = KIND == kPoly ? b * o + c * v[e] : a * o + v[e];
-        }
-      }
-      if constexpr (KIND != kApply || !LAST) {
-        if (row < j.m && col_in) put8(D + (int64_t)row * ld + c0, plane, KIND == kApply || SPLIT, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= kInvScale;
-        if (!j.tall && row < j.m) finish8(j, (int64_t)row * j.n, c0, j.n, v);
-      }
-      if (back) {
-        *reinterpret_cast<f4*>(mine) = f4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f4*>(mine + 4) = f4{v[4], v[5], v[6], v[7]};
-      }
-    }
-    if (back) {
-      wave_sync();
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int cc = p * 16 + (lane >> 2), rr = (lane & 3) * 8, col = n0 + wn * 64 + cc, row = r0 + rr;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = turn[(rr + e) * kTurn + cc];
-        if constexpr (KIND != kApply) {
-          if (col < j.m) put8(D + (int64_t)col * ld + row, plane, SPLIT, v);
-        } else if constexpr (LAST) {
-          if (col < j.n) finish8(j, (int64_t)col * j.m, row, j.m, v);
-        }
-      }
-    }
-    wave_sync();   // the block has been read
   }
+  // A wave's accumulators go out 32 rows x 64 columns at a time.
+  float* const turn = reinterpret_cast<float*>(smem) + wave * (32 * kTurn);
+  constexpr int Q = T::BN < T::BM ? 1 : T::BN / T::BM;
+  const bool mirror = KIND != kApply && tn != tm / Q;
+  [&]<int... I>(std::integer_sequence<int, I...>) __attribute__((always_inline)) {
+    (
+        [&]() __attribute__((always_inline)) {
+          constexpr int s = I / (T::TN / 2), t = I % (T::TN / 2) * 2;
+          finish<KIND, SPLIT, LAST, ADD>(j, st, mirror, m0 + wm * T::WM + s * 32, n0 + wn * T::WN + t * 32, acc[s][t],
+                                         acc[s][t + 1], turn, lane);
+          __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
+        }(),
+        ...);
+  }(std::make_integer_sequence<int, T::TM * T::TN / 2>{});
+}
+
+// Adds up the shares of split reductions, in their order, 32 x 64 a wave.
+template <bool SPLIT, class T>
+__global__ __launch_bounds__(64 * T::WAVES) void ns_join_kernel(Jobs jobs, Step st) {
+  __shared__ __align__(16) float smem[T::WAVES * 32 * kTurn];
+  const Job& j = job_of(jobs, blockIdx.x);
+  const int splits = j.gram_splits;
+  if (splits <= 1) return;
+  constexpr int PAIRS = T::TM * T::TN / 2;   // of a wave's tile, and workgroups of a tile
+  const int k = (blockIdx.x - j.first) / PAIRS;
+  const int pair = (blockIdx.x - j.first) % PAIRS, s = pair / (T::TN / 2), t = pair % (T::TN / 2) * 2;
+  constexpr int FLOATS = T::BM * T::BN;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float* p = j.partial + (int64_t)k * splits * FLOATS + wave * (FLOATS / T::WAVES) + (s * T::TN + t) * 1024 + lane * 4;
+  int tm, tn;
+  upper_tile<T>(j.m, k, tm, tn);
+  f16v acc[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[h][e] = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < splits; ++i, p += FLOATS) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const f4 v = *reinterpret_cast<const f4*>(p + q * 256);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[q >> 2][4 * (q & 3) + e] += v[e];
+    }
+  }
+  finish<kGram, SPLIT, false, false>(j, st, tn != tm / (T::BN / T::BM), tm * T::BM + wave % T::WAVES_M * T::WM + s * 32,
+                             tn * T::BN + wave / T::WAVES_M * T::WN + t * 32, acc[0], acc[1], smem + wave * (32 * kTurn), lane);
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// The tiles.  Square, for A and for all last products too small for the others:
+// three of its workgroups share a CU when the products are rounded, one when
+// they are split.  Small, for B, whose short reduction wants more workgroups: one
+// 1600 x 1600 takes 16 us in 181 of them and 20 us in 91 squares.  Tall and Broad,
+// for last products, read fewer bytes a product.
+template <bool SPLIT> using Square = Tile<128, 128, 64, 64, 3, SPLIT ? 1 : 3>;
+template <bool SPLIT> using Small = Tile<64, 128, 32, 64, SPLIT ? 3 : 4, SPLIT ? 2 : 3>;
+using Tall = Tile<320, 256, 160, 64, 4, 2>;
+using Broad = Tile<128, 256, 64, 64, 3, 2>;
+
+// Items per tile of a reduction over K for a launch of `tiles` tiles: enough
+// to put per_cu on every CU, none shorter than kMinStages.
+constexpr int kMinStages = 8;
+int splits_for(int64_t tiles, int per_cu, int K) {
+  const int64_t want = (int64_t)per_cu * device_cu_count() / tiles, most = K / (kMinStages * kBK);
+  const int64_t n = want < most ? want : most;
+  return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
 
 // Bytes of one weight's workspace; fills its pointers when base is given.
 int64_t lay_out(Job& j, unsigned char* base) {
@@ -557,16 +789,18 @@ int64_t lay_out(Job& j, unsigned char* base) {
     at += up(bytes, 256);
     return p;
   };
-  const int64_t x = (int64_t)j.m * j.ldx * 4, a = (int64_t)j.m * j.lda * 4;   // two parts of 2 bytes
+  const int64_t x = (int64_t)j.na * j.nx * 4096, a = (int64_t)j.na * j.na * 4096;   // two parts of 2 bytes
   j.sums = reinterpret_cast<double*>(take(kMaxParts * 8));
   j.x[0] = reinterpret_cast<_Float16*>(take(x));
   j.x[1] = reinterpret_cast<_Float16*>(take(x));
   j.A = reinterpret_cast<_Float16*>(take(a));
   j.B = reinterpret_cast<_Float16*>(take(a));
+  const int splits = j.gram_splits;
+  j.partial = reinterpret_cast<float*>(take(splits > 1 ? upper_tiles<Square<false>>(j.m) * splits * Square<false>::BM * Square<false>::BN * 4 : 0));
   return at;
 }
 
-int64_t fill(Jobs& jobs, const NsJob* in, int count, unsigned char* ws) {
+int64_t fill(Jobs& jobs, const NsJob* in, int count, bool split, unsigned char* ws) {
   int64_t at = 0;
   jobs.count = 0;
   for (int k = 0; k < count; ++k) {
@@ -584,12 +818,18 @@ int64_t fill(Jobs& jobs, const NsJob* in, int count, unsigned char* ws) {
     j.tall = s.R > s.C;
     j.m = (int)(j.tall ? s.C : s.R);
     j.n = (int)(j.tall ? s.R : s.C);
-    j.lda = (int)up(j.m, 64);
-    j.ldx = (int)up(j.n, 64);
+    j.na = (j.m + 31) / 32;
+    j.nx = (j.n + 31) / 32;
     const int64_t parts = ((int64_t)j.m * j.n + kNormChunk - 1) / kNormChunk;
     j.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
     j.g32 = s.g32;
     j.out32 = s.out32;
+  }
+  int64_t tiles = 0;
+  for (int k = 0; k < jobs.count; ++k) tiles += upper_tiles<Square<false>>(jobs.j[k].m);
+  for (int k = 0; k < jobs.count; ++k) {
+    Job& j = jobs.j[k];
+    j.gram_splits = splits_for(tiles, split ? 1 : 2, 32 * j.nx);
     at += lay_out(j, ws ? ws + at : nullptr);
   }
   return at;
@@ -606,38 +846,87 @@ unsigned deal(Jobs& jobs, F blocks) {
   return (unsigned)at;
 }
 
+template <int KIND, bool SPLIT, bool LAST, bool ADD, class T>
+void product(Jobs& jobs, const Step& st, hipStream_t s) {
+  const unsigned grid = deal(jobs, [](const Job& j) {
+    if constexpr (KIND == kApply)
+      return up(up(j.m, T::BM) / T::BM * (up(j.n, T::BN) / T::BN), 8);
+    else
+      return up(upper_tiles<T>(j.m) * (KIND == kGram ? j.gram_splits : 1), 8);
+  });
+  hipLaunchKernelGGL((ns_product_kernel<KIND, SPLIT, LAST, ADD, T>), dim3(grid), dim3(64 * T::WAVES), 0, s, jobs, st);
+  if constexpr (KIND == kGram) {
+    const unsigned blocks =
+        deal(jobs, [](const Job& j) { return j.gram_splits > 1 ? upper_tiles<T>(j.m) * (T::TM * T::TN / 2) : 0; });
+    if (blocks > 0) hipLaunchKernelGGL((ns_join_kernel<SPLIT, T>), dim3(blocks), dim3(64 * T::WAVES), 0, s, jobs, st);
+  }
+}
+
+template <class T>
+int64_t apply_tiles(const Jobs& jobs) {
+  int64_t t = 0;
+  for (int k = 0; k < jobs.count; ++k) t += up(jobs.j[k].m, T::BM) / T::BM * (up(jobs.j[k].n, T::BN) / T::BN);
+  return t;
+}
+
+template <bool SPLIT, class T>
+void apply(Jobs& jobs, const Step& st, bool last, hipStream_t s) {
+  if (last && st.in_q)
+    product<kApply, SPLIT, true, false, T>(jobs, st, s);
+  else if (st.in_q)
+    product<kApply, SPLIT, false, false, T>(jobs, st, s);
+  else if constexpr (!SPLIT) {
+    if (last)
+      product<kApply, SPLIT, true, true, T>(jobs, st, s);
+    else
+      product<kApply, SPLIT, false, true, T>(jobs, st, s);
+  }
+}
+
 template <bool SPLIT>
 void step(Jobs& jobs, const NsParams& prm, int k, hipStream_t s) {
-  const float a = prm.coef[3 * k], b = prm.coef[3 * k + 1], c = prm.coef[3 * k + 2];
-  const int cur = k & 1;
-  const bool lo = k < kLoSteps;
-  const unsigned square = deal(jobs, [](const Job& j) {
-    const int64_t t = up(j.m, kTile) / kTile;
-    return t * (t + 1) / 2;
-  });
-  hipLaunchKernelGGL((ns_product_kernel<kGram, SPLIT, false>), dim3(square), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
-  hipLaunchKernelGGL((ns_product_kernel<kPoly, SPLIT, false>), dim3(square), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
-  const unsigned wide = deal(jobs, [](const Job& j) { return up(up(j.m, kTile) / kTile * (up(j.n, kTile) / kTile), 8); });
-  if (k + 1 < prm.steps)
-    hipLaunchKernelGGL((ns_product_kernel<kApply, SPLIT, false>), dim3(wide), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
-  else
-    hipLaunchKernelGGL((ns_product_kernel<kApply, SPLIT, true>), dim3(wide), dim3(kThreads), 0, s, jobs, cur, a, b, c, lo);
+  const Step st{k & 1, prm.coef[3 * k], prm.coef[3 * k + 1], prm.coef[3 * k + 2], SPLIT || k >= kLoSteps,
+                SPLIT || k + 1 < kLoSteps};
+  product<kGram, SPLIT, false, false, Square<SPLIT>>(jobs, st, s);
+  product<kPoly, SPLIT, false, false, Small<SPLIT>>(jobs, st, s);
+  const bool last = k + 1 == prm.steps;
+  // The larger tile where its whole rounds over the CUs cost less, by area over
+  // measured speed.  Rounded products: two 1600 x 6400 weights take 65 us in 250
+  // Tall tiles and 80 us in 1300 Square ones, one weight 52 and 41 us (the
+  // squares, three to a CU, are taken to fill the CUs evenly).  Split ones: 1024
+  // x 4096 and its transpose take 51 us in 256 Broad tiles, 59 us in 512 Square
+  // ones.
+  const int64_t cus = device_cu_count();
+  const int64_t squares = apply_tiles<Square<SPLIT>>(jobs);
+  if constexpr (SPLIT) {
+    const int64_t rounds = (apply_tiles<Broad>(jobs) + cus - 1) / cus;
+    if (rounds * 2 * 6 < (squares + cus - 1) / cus * 7)
+      apply<SPLIT, Broad>(jobs, st, last, s);
+    else
+      apply<SPLIT, Square<SPLIT>>(jobs, st, last, s);
+  } else {
+    const int64_t rounds = (apply_tiles<Tall>(jobs) + cus - 1) / cus;
+    if (rounds * 5 * 5 * cus < squares * 6)
+      apply<SPLIT, Tall>(jobs, st, last, s);
+    else
+      apply<SPLIT, Square<SPLIT>>(jobs, st, last, s);
+  }
 }
 
 }  // namespace
 
 int64_t ns_workspace(const NsJob* jobs, int count) {
   Jobs j{};
-  return fill(j, jobs, count, nullptr);
+  return fill(j, jobs, count, false, nullptr);
 }
 
 hipError_t launch_newton_schulz(const NsJob* in, int count, const NsParams& prm, void* ws, hipStream_t s) {
   Jobs jobs{};
-  fill(jobs, in, count, static_cast<unsigned char*>(ws));
+  fill(jobs, in, count, prm.split, static_cast<unsigned char*>(ws));
   if (jobs.count == 0) return hipSuccess;
   const unsigned norm = deal(jobs, [](const Job& j) { return (int64_t)j.parts; });
   hipLaunchKernelGGL(ns_norm_kernel, dim3(norm), dim3(kThreads), 0, s, jobs, prm.mu, prm.nesterov);
-  const unsigned start = deal(jobs, [](const Job& j) { return up(j.m, 64) / 64 * (int64_t)(j.ldx / 64); });
+  const unsigned start = deal(jobs, [](const Job& j) { return (int64_t)j.na * ((j.nx + 1) / 2); });
   hipLaunchKernelGGL(ns_start_kernel, dim3(start), dim3(kThreads), 0, s, jobs, prm.mu, prm.nesterov, prm.eps);
   for (int k = 0; k < prm.steps; ++k) {
     if (prm.split)
