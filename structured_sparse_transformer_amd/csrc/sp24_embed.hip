@@ -52,6 +52,7 @@ __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(const Id* __restric
   const int64_t first = (int64_t)blockIdx.x * (kThreads * kItems);
   const int64_t t0 = first / chunks;
   const uint32_t c0 = (uint32_t)(first - t0 * chunks);
+  // no branches around the loads: kItems gathers are in flight
   int64_t t[kItems], id[kItems];
   uint32_t c[kItems];
 #pragma unroll
@@ -60,22 +61,27 @@ __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(const Id* __restric
     const uint32_t q = i / chunks;
     t[k] = t0 + q;
     c[k] = i - q * chunks;
-    id[k] = t[k] < T ? (int64_t)ids[t[k]] : -1;
+    id[k] = (int64_t)ids[min<int64_t>(t[k], T - 1)];
   }
   float v[kItems][VEC];
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
+  for (int k = 0; k < kItems; ++k)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[k][e] = 0.0f;
-    if (id[k] >= 0 && id[k] < V) {
-      const Table* row = table + id[k] * d + (int64_t)c[k] * VEC;
+  if (V > 0) {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int64_t r = id[k] >= 0 && id[k] < V ? id[k] : 0;
+      const Table* row = table + r * d + (int64_t)c[k] * VEC;
       if constexpr (VEC == 8)
         load_row8<Table>(row, v[k]);
       else
         v[k][0] = (float)row[0];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[k][e] *= scale;
     }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[k][e] = id[k] >= 0 && id[k] < V ? v[k][e] * scale : 0.0f;
   }
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
@@ -112,17 +118,21 @@ hipError_t launch_fwd(const void* ids, const void* table, int64_t T, int64_t V, 
 // Gradient: stable counting sort by id, then sums of runs.
 //
 // The ids are dealt in ranges of kRange to workgroups of kWaves waves, and the
-// tokens in at most kMaxSegs segments of a multiple of kSegStep.  A workgroup
-// reads all ids of its segment and keeps those of its range; each wave has a
+// tokens in at most kMaxSegs segments, kMinSeg tokens long or more.  A workgroup
+// keeps those tokens of its segment that are in its range; each wave has a
 // contiguous part of the segment and its own counters, so that tokens of one
 // id are placed in token order.
-//   count: cnt[seg][v] and below[seg][range], the segment's tokens of each id
-//          and with ids below the range
 //   place: start[v], where id v's run begins in sorted order, and
 //          sorted[p] = (token, id)
-constexpr int kRange = 1024, kWaves = kRange / 64, kSegStep = 4096, kMaxSegs = 32;
-constexpr int kGroups = kSegStep / kWaves / 64;   // groups of 64 tokens that a wave loads at once
-static_assert(kGroups * kWaves * 64 == kSegStep, "whole waves of tokens");
+// For that it needs the number of tokens of each of its ids, in earlier
+// segments and in all, and of those with ids below its range.  Up to
+// kSelfCount tokens every workgroup counts them itself (16384 tokens are 128
+// KiB from L2, less than a launch); beyond, a kernel before it does, once a
+// segment:
+//   count: cnt[seg][v] and below[seg][range]
+constexpr int kRange = 1024, kWaves = kRange / 64, kMinSeg = 2048, kMaxSegs = 16, kSelfCount = 32768;
+constexpr int kGroups = 4;   // groups of 64 tokens that a wave loads at once
+static_assert(kMinSeg % (64 * kWaves) == 0, "whole waves of tokens");
 
 // What one lane of a wave has written to LDS is read by the others.
 __device__ __forceinline__ void wave_sync() {
@@ -130,78 +140,119 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// The id of token t relative to the range [lo, lo + kRange); -1 for one below
-// it, kRange for one above or padding.
+// Token t's id; past the end and for every id beyond 32 bits, the largest
+// number, which is no id (V < 2^31).  Scanning is the sort's work: every id is
+// looked at once a range, in a few 32-bit operations, and without a branch, so
+// that several loads are in flight.  end > 0.
+__device__ __forceinline__ uint32_t id_at(const int32_t* ids, int t, int end) {
+  const uint32_t w = (uint32_t)ids[min(t, end - 1)];
+  return t < end ? w : ~0u;
+}
+__device__ __forceinline__ uint32_t id_at(const int64_t* ids, int t, int end) {
+  const uint2 w = reinterpret_cast<const uint2*>(ids)[min(t, end - 1)];
+  return t < end && w.y == 0 ? w.x : ~0u;
+}
+
+// Counts the tokens t0 .. end - 1 of the range's ids into n; returns, in
+// every lane, how many of the wave's were below the range.
 template <typename Id>
-__device__ __forceinline__ int in_range(const Id* ids, int64_t t, int64_t end, int64_t lo, int64_t V) {
-  if (t >= end) return kRange;
-  const int64_t id = (int64_t)ids[t];
-  if (id < 0 || id >= V) return kRange;
-  if (id < lo) return -1;
-  return id - lo < kRange ? (int)(id - lo) : kRange;
+__device__ __forceinline__ int count_tokens(const Id* ids, int t0, int end, uint32_t lo, uint32_t span, int32_t* n) {
+  int under = 0;
+  constexpr int kLoads = 8;
+  for (int t = t0; t < end; t += kLoads * kRange) {
+    uint32_t v[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) v[k] = id_at(ids, t + k * kRange + threadIdx.x, end);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      if (v[k] - lo < span) atomicAdd(&n[v[k] - lo], 1);
+      under += __popcll(__ballot(v[k] < lo));
+    }
+  }
+  return under;
 }
 
 template <typename Id>
-__global__ __launch_bounds__(kRange) void embed_count_kernel(const Id* __restrict__ ids, int64_t T, int64_t V,
-                                                             int64_t seg_tokens, int32_t* __restrict__ cnt,
+__global__ __launch_bounds__(kRange) void embed_count_kernel(const Id* __restrict__ ids, int T, int64_t V,
+                                                             int seg_tokens, int32_t* __restrict__ cnt,
                                                              int32_t* __restrict__ below) {
   __shared__ int32_t n[kRange];
   __shared__ int32_t under;
   const int tid = threadIdx.x;
-  const int64_t range = blockIdx.x, seg = blockIdx.y, lo = range * kRange;
+  const int64_t range = blockIdx.x;
+  const int seg = blockIdx.y;
+  const uint32_t lo = (uint32_t)(range * kRange), span = (uint32_t)min<int64_t>(kRange, V - lo);
   n[tid] = 0;
   if (tid == 0) under = 0;
   __syncthreads();
-  const int64_t end = min<int64_t>((seg + 1) * seg_tokens, T);
-  int mine = 0;
-  for (int64_t t = seg * seg_tokens; t < end; t += kSegStep) {
-#pragma unroll
-    for (int k = 0; k < kSegStep / kRange; ++k) {
-      const int v = in_range(ids, t + k * kRange + tid, end, lo, V);
-      if (v >= 0 && v < kRange) atomicAdd(&n[v], 1);
-      mine += __popcll(__ballot(v < 0));   // the wave's count, in every lane
-    }
-  }
+  const int mine = count_tokens(ids, seg * seg_tokens, min(T, (seg + 1) * seg_tokens), lo, span, n);
   if ((tid & 63) == 0) atomicAdd(&under, mine);
   __syncthreads();
   cnt[(seg * gridDim.x + range) * kRange + tid] = n[tid];
   if (tid == 0) below[seg * gridDim.x + range] = under;
 }
 
-template <typename Id>
-__global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restrict__ ids, int64_t T, int64_t V,
-                                                             int64_t seg_tokens, const int32_t* __restrict__ cnt,
+template <typename Id, bool SELF>
+__global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restrict__ ids, int T, int64_t V,
+                                                             int seg_tokens, const int32_t* __restrict__ cnt,
                                                              const int32_t* __restrict__ below,
                                                              int32_t* __restrict__ start, int2* __restrict__ sorted) {
   __shared__ int32_t n[kWaves][kRange];   // counts of each wave's tokens, then where its next one goes
-  __shared__ int32_t wave_sum[kWaves];
+  __shared__ int32_t others[SELF ? 2 : 1][kRange];
+  __shared__ int32_t wave_sum[kWaves], under;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t range = blockIdx.x, seg = blockIdx.y, ranges = gridDim.x, segs = gridDim.y, lo = range * kRange;
+  const int64_t range = blockIdx.x, ranges = gridDim.x;
+  const int seg = blockIdx.y, segs = gridDim.y;
+  const uint32_t lo = (uint32_t)(range * kRange), span = (uint32_t)min<int64_t>(kRange, V - lo);
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) n[w][tid] = 0;
+  if constexpr (SELF) {
+    others[0][tid] = others[1][tid] = 0;
+    if (tid == 0) under = 0;
+  }
   __syncthreads();
-  const int64_t per_wave = seg_tokens / kWaves;
-  const int64_t t0 = seg * seg_tokens + wave * per_wave, end = min<int64_t>(t0 + per_wave, T);
-  int v[kGroups];
-  auto load = [&](int64_t t) {
+  const int per_wave = seg_tokens / kWaves;
+  const int t0 = seg * seg_tokens + wave * per_wave, end = min(t0 + per_wave, T);
+  uint32_t v[kGroups];
+  auto load = [&](int t) {
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) v[k] = in_range(ids, t + k * 64 + lane, end, lo, V);
+    for (int k = 0; k < kGroups; ++k) v[k] = id_at(ids, t + k * 64 + lane, end);
   };
-  for (int64_t t = t0; t < end; t += kGroups * 64) {
+  int mine = 0;
+  for (int t = t0; t < end; t += kGroups * 64) {
     load(t);
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k)
-      if (v[k] >= 0 && v[k] < kRange) atomicAdd(&n[wave][v[k]], 1);
+    for (int k = 0; k < kGroups; ++k) {
+      if (v[k] - lo < span) atomicAdd(&n[wave][v[k] - lo], 1);
+      if constexpr (SELF) mine += __popcll(__ballot(v[k] < lo));
+    }
   }
-  // this thread's id over all segments, the earlier ones apart
-  int total = 0, before = 0;
-  for (int64_t s = 0; s < segs; ++s) {
-    const int c = cnt[(s * ranges + range) * kRange + tid];
-    total += c;
-    if (s < seg) before += c;
+  // this thread's id in the segments before and in all
+  int total = 0, before = 0, base = 0;
+  if constexpr (SELF) {
+    mine += count_tokens(ids, 0, min(T, seg * seg_tokens), lo, span, others[0]);
+    mine += count_tokens(ids, (seg + 1) * seg_tokens, T, lo, span, others[1]);
+    if (lane == 0) atomicAdd(&under, mine);
+    __syncthreads();
+    before = others[0][tid];
+    total = before + others[1][tid];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) total += n[w][tid];
+    base = under;
+  } else {
+    int c[kMaxSegs], u[kMaxSegs];   // all loads in flight
+#pragma unroll
+    for (int s = 0; s < kMaxSegs; ++s) {
+      c[s] = s < segs ? cnt[(s * ranges + range) * kRange + tid] : 0;
+      u[s] = s < segs ? below[s * ranges + range] : 0;
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxSegs; ++s) {
+      total += c[s];
+      if (s < seg) before += c[s];
+      base += u[s];
+    }
   }
-  int base = 0;
-  for (int64_t s = 0; s < segs; ++s) base += below[s * ranges + range];
   // exclusive scan of the totals over the range's ids
   int incl = total;
 #pragma unroll
@@ -213,9 +264,9 @@ __global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restric
   __syncthreads();   // the wave counts are complete as well
   for (int w = 0; w < wave; ++w) base += wave_sum[w];
   const int first = base + incl - total;
-  if (seg == 0 && lo + tid < V) {
+  if (seg == 0 && tid < (int)span) {
     start[lo + tid] = first;
-    if (lo + tid == V - 1) start[V] = first + total;
+    if ((int64_t)lo + tid == V - 1) start[V] = first + total;
   }
   int run = first + before;
 #pragma unroll
@@ -225,153 +276,204 @@ __global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restric
     run += c;
   }
   __syncthreads();
-  for (int64_t t = t0; t < end; t += kGroups * 64) {
+  for (int t = t0; t < end; t += kGroups * 64) {
     load(t);
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-      const bool in = v[k] >= 0 && v[k] < kRange;
+      const uint32_t i = v[k] - lo;
+      const bool in = i < span;
       uint64_t same = __ballot(in);
       if (same == 0) continue;
       // lanes with this lane's id, by one ballot a bit
 #pragma unroll
       for (int b = 0; b < 10; ++b) {
-        const bool bit = (v[k] >> b) & 1;
+        const bool bit = (i >> b) & 1;
         const uint64_t set = __ballot(bit);
         same &= bit ? set : ~set;
       }
       const int rank = __popcll(same & ((1ull << lane) - 1));
-      if (in) sorted[n[wave][v[k]] + rank] = make_int2((int)(t + k * 64 + lane), (int)(lo + v[k]));
+      if (in) sorted[n[wave][i] + rank] = make_int2(t + k * 64 + lane, (int)v[k]);
       wave_sync();   // every lane has read its counter
-      if (in && rank == 0) n[wave][v[k]] += __popcll(same);
+      if (in && rank == 0) n[wave][i] += __popcll(same);
       wave_sync();
     }
   }
 }
 
-// Sums of runs.  The sorted tokens are cut into chunks of kChunk; a team of
-// threads sums a chunk's rows in order, kVec columns a thread.  A run inside
-// one chunk goes to its row of the gradient.  A run that came from the chunk
-// before leaves its part in head[chunk], one that starts here and goes on in
-// tail[chunk]; embed_join_kernel adds those.
-constexpr int kChunk = 64, kAhead = 8;
+// Sums of runs.  The sorted tokens are cut into chunks; a team of threads sums
+// a chunk's rows in order, VEC columns a thread, kAhead rows in flight.  A run
+// inside one chunk goes to its row of the gradient.  A run that came from the
+// chunk before leaves its part in parts[2 chunk], one that starts here and goes
+// on in parts[2 chunk + 1]; embed_join_kernel adds those.  The workgroups past
+// the chunks' clear the rows of ids that no token has, kClearRows each, so that
+// these writes run beside the sums' reads.
+constexpr int kAhead = 8, kClearRows = 16;
 
+// VEC values of a row of dout; read once, so they need not stay in the caches
+// (74 to 61 us for 16384 rows of 1600 beside the writes of 322 MB).
 template <int VEC>
-__device__ __forceinline__ void add_row(const _Float16* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const h8 x = *reinterpret_cast<const h8*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
-  } else {
-    v[0] = (float)p[0];
-  }
-}
+struct Row;
+template <>
+struct Row<8> {
+  h8 x;
+  __device__ __forceinline__ void load(const _Float16* p) { x = __builtin_nontemporal_load(reinterpret_cast<const h8*>(p)); }
+  __device__ __forceinline__ float at(int e) const { return (float)x[e]; }
+};
+template <>
+struct Row<1> {
+  _Float16 x;
+  __device__ __forceinline__ void load(const _Float16* p) { x = *p; }
+  __device__ __forceinline__ float at(int) const { return (float)x; }
+};
 
+// VEC values of fp32, 16 bytes at a time
 template <int VEC>
-__device__ __forceinline__ void store_sum(float* p, const float (&v)[VEC], float scale, bool add) {
+__device__ __forceinline__ void load_sum(const float* p, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
-    f4 x, y;
+    const f4 x = *reinterpret_cast<const f4*>(p), y = *reinterpret_cast<const f4*>(p + 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[e] = v[e] * scale;
-      y[e] = v[4 + e] * scale;
+      v[e] = x[e];
+      v[4 + e] = y[e];
     }
-    if (add) {
-      x += *reinterpret_cast<const f4*>(p);
-      y += *reinterpret_cast<const f4*>(p + 4);
-    }
-    *reinterpret_cast<f4*>(p) = x;
-    *reinterpret_cast<f4*>(p + 4) = y;
   } else {
-    p[0] = add ? p[0] + v[0] * scale : v[0] * scale;
+    v[0] = p[0];
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_sum(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    *reinterpret_cast<f4*>(p) = f4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f4*>(p + 4) = f4{v[4], v[5], v[6], v[7]};
+  } else {
+    p[0] = v[0];
   }
 }
 
-// blockIdx.x: teams of chunks; blockIdx.y: slices of team * VEC columns
-template <int VEC>
+// blockIdx.x: teams of chunks, then the rows to clear; blockIdx.y: slices of
+// team * VEC columns.  With ADD the gradient's old values are loaded with the
+// rows that end their runs: loaded at the end of each run, one after the other,
+// they made up most of the kernel's time.
+template <int VEC, bool ADD>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const int2* __restrict__ sorted,
                                                              const int32_t* __restrict__ start,
                                                              const _Float16* __restrict__ dout, int64_t V, int64_t d,
-                                                             float scale, int team, int add, float* __restrict__ parts,
-                                                             float* __restrict__ dtable) {
+                                                             float scale, int team, int chunk_tokens, int sum_blocks,
+                                                             float* __restrict__ parts, float* __restrict__ dtable) {
+  if ((int)blockIdx.x >= sum_blocks) {
+    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * kClearRows, v1 = min<int64_t>(v0 + kClearRows, V);
+    const int64_t c0 = (int64_t)blockIdx.y * team * VEC, c1 = min<int64_t>(c0 + team * VEC, d);
+    for (int64_t v = v0; v < v1; ++v) {
+      if (start[v] != start[v + 1]) continue;
+      if constexpr (VEC == 8) {
+        for (int64_t c = c0 + threadIdx.x * 4; c < c1; c += kThreads * 4) *reinterpret_cast<f4*>(dtable + v * d + c) = f4{};
+      } else {
+        for (int64_t c = c0 + threadIdx.x; c < c1; c += kThreads) dtable[v * d + c] = 0.0f;
+      }
+    }
+    return;
+  }
   const int total = start[V];
   const int64_t chunk = (int64_t)blockIdx.x * (kThreads / team) + threadIdx.x / team;
   const int64_t col = ((int64_t)blockIdx.y * team + threadIdx.x % team) * VEC;
-  const int64_t p0 = chunk * kChunk;
+  const int64_t p0 = chunk * chunk_tokens;
   if (p0 >= total || col >= d) return;
-  const int count = (int)min<int64_t>(kChunk, total - p0);
-  const bool from_before = p0 > 0 && sorted[p0 - 1].y == sorted[p0].y;
-  const bool goes_on = p0 + count < total && sorted[p0 + count].y == sorted[p0 + count - 1].y;
+  const int count = (int)min<int64_t>(chunk_tokens, total - p0);
+  const int id_before = p0 > 0 ? sorted[p0 - 1].y : -1, id_after = p0 + count < total ? sorted[p0 + count].y : -1;
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
-  int id = sorted[p0].y;
-  bool first = true;   // still in the chunk's first run
+  int2 at[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) at[k] = sorted[p0 + min(k, count - 1)];
+  bool head = at[0].y == id_before;   // in a run that came from the chunk before
   for (int i = 0; i < count; i += kAhead) {
-    int2 at[kAhead];
-    float v[kAhead][VEC];
+    Row<VEC> v[kAhead];
+    float old[ADD ? kAhead : 1][VEC];
+    int ids[kAhead + 1];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) at[k] = sorted[p0 + min(i + k, count - 1)];
+    for (int k = 0; k < kAhead; ++k) {
+      v[k].load(dout + (int64_t)at[k].x * d + col);
+      ids[k] = at[k].y;
+    }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) add_row<VEC>(dout + (int64_t)at[k].x * d + col, v[k]);
+    for (int k = 0; k < kAhead; ++k) at[k] = sorted[p0 + min(i + kAhead + k, count - 1)];
+    ids[kAhead] = at[0].y;
+    bool ends[kAhead];   // row i + k is its run's last, or the chunk's
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      ends[k] = i + k + 1 >= count || ids[k + 1] != ids[k];
+      if (ADD && ends[k] && i + k < count) load_sum<VEC>(dtable + (int64_t)ids[k] * d + col, old[ADD ? k : 0]);
+    }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (i + k >= count) break;
-      if (at[k].y != id) {
-        if (first && from_before)
-          store_sum<VEC>(parts + (2 * chunk) * d + col, acc, 1.0f, false);
-        else
-          store_sum<VEC>(dtable + (int64_t)id * d + col, acc, scale, add != 0);
-        first = false;
-        id = at[k].y;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
+      for (int e = 0; e < VEC; ++e) acc[e] += v[k].at(e);
+      if (!ends[k]) continue;
+      if (head) {
+        store_sum<VEC>(parts + 2 * chunk * d + col, acc);
+      } else if (i + k + 1 >= count && ids[k] == id_after) {
+        store_sum<VEC>(parts + (2 * chunk + 1) * d + col, acc);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = ADD ? old[ADD ? k : 0][e] + acc[e] * scale : acc[e] * scale;
+        store_sum<VEC>(dtable + (int64_t)ids[k] * d + col, acc);
       }
+      head = false;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] += v[k][e];
+      for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
     }
   }
-  if (first && from_before)
-    store_sum<VEC>(parts + (2 * chunk) * d + col, acc, 1.0f, false);
-  else if (goes_on)
-    store_sum<VEC>(parts + (2 * chunk + 1) * d + col, acc, 1.0f, false);
-  else
-    store_sum<VEC>(dtable + (int64_t)id * d + col, acc, scale, add != 0);
 }
 
-// The chunk in which a run that goes on has started adds up its parts, in
-// order.  One thread a column.
-__global__ __launch_bounds__(kThreads) void embed_join_kernel(const int2* __restrict__ sorted,
-                                                              const int32_t* __restrict__ start, int64_t V, int64_t d,
-                                                              float scale, int add, const float* __restrict__ parts,
-                                                              float* __restrict__ dtable) {
+// Of the chunk in which a run that goes on has started, adds up the run's
+// parts: every wave takes every kJoinWaves-th part after the first, in order,
+// and the waves' sums are added in theirs.  256 columns a workgroup.
+constexpr int kJoinWaves = 8;
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const int2* __restrict__ sorted,
+                                                                     const int32_t* __restrict__ start, int64_t V,
+                                                                     int64_t d, float scale, int chunk_tokens, int add,
+                                                                     const float* __restrict__ parts,
+                                                                     float* __restrict__ dtable) {
+  __shared__ float sums[kJoinWaves][256];
   const int total = start[V];
-  const int64_t chunk = blockIdx.x, last = (chunk + 1) * kChunk - 1;
+  const int64_t chunk = blockIdx.x, last = (chunk + 1) * chunk_tokens - 1;
   if (last + 1 >= total) return;
   const int id = sorted[last].y;
-  if (sorted[last + 1].y != id || start[id] < chunk * kChunk) return;
-  const int64_t end = (start[id + 1] - 1) / kChunk;
-  for (int64_t c = threadIdx.x; c < d; c += kThreads) {
-    float v = parts[(2 * chunk + 1) * d + c];
-    for (int64_t k = chunk + 1; k <= end; ++k) v += parts[2 * k * d + c];
-    v *= scale;
-    float* o = dtable + (int64_t)id * d + c;
-    *o = add ? *o + v : v;
+  if (sorted[last + 1].y != id || start[id] < chunk * chunk_tokens) return;
+  const int64_t end = (start[id + 1] - 1) / chunk_tokens;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c0 = (int64_t)blockIdx.y * 256 + lane;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto part = [&](int64_t row, float (&x)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = c0 + 64 * e < d ? parts[row * d + c0 + 64 * e] : 0.0f;
+  };
+  if (wave == 0) part(2 * chunk + 1, v);
+#pragma unroll 4
+  for (int64_t k = chunk + 1 + wave; k <= end; k += kJoinWaves) {
+    float x[4];
+    part(2 * k, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += x[e];
   }
-}
-
-// Rows of ids that no token has, kClearRows a workgroup.
-constexpr int kClearRows = 16;
-__global__ __launch_bounds__(kThreads) void embed_clear_kernel(const int32_t* __restrict__ start, int64_t V, int64_t d,
-                                                               float* __restrict__ dtable) {
-  const int64_t v0 = (int64_t)blockIdx.x * kClearRows, v1 = min<int64_t>(v0 + kClearRows, V);
-  for (int64_t v = v0; v < v1; ++v) {
-    if (start[v] != start[v + 1]) continue;
-    for (int64_t c = threadIdx.x; c < d; c += kThreads) dtable[v * d + c] = 0.0f;
-  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sums[wave][lane + 64 * e] = v[e];
+  __syncthreads();
+  const int c = threadIdx.x;
+  const int64_t col = (int64_t)blockIdx.y * 256 + c;
+  if (c >= 256 || col >= d) return;
+  float s = sums[0][c];
+#pragma unroll
+  for (int w = 1; w < kJoinWaves; ++w) s += sums[w][c];
+  s *= scale;
+  float* o = dtable + (int64_t)id * d + col;
+  *o = add ? *o + s : s;
 }
 
 struct BwdPlan {
-  int64_t ranges, segs, seg_tokens, chunks;
+  int64_t ranges, segs, seg_tokens, chunk_tokens, chunks;
   int64_t cnt, below, start, sorted, parts, bytes;   // byte offsets in the workspace
 };
 
@@ -379,10 +481,14 @@ BwdPlan bwd_plan(int64_t T, int64_t V, int64_t d) {
   BwdPlan p;
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   p.ranges = (V + kRange - 1) / kRange;
-  p.seg_tokens = (T + (int64_t)kMaxSegs * kSegStep - 1) / ((int64_t)kMaxSegs * kSegStep) * kSegStep;
-  if (p.seg_tokens == 0) p.seg_tokens = kSegStep;
+  const int64_t unit = 64 * kWaves;
+  p.seg_tokens = (T + kMaxSegs * unit - 1) / (kMaxSegs * unit) * unit;
+  if (p.seg_tokens < kMinSeg) p.seg_tokens = kMinSeg;
   p.segs = T == 0 ? 1 : (T + p.seg_tokens - 1) / p.seg_tokens;
-  p.chunks = (T + kChunk - 1) / kChunk;
+  // shorter chunks where there are few: 517 tokens' sums wait for 16 rows each,
+  // not for 64; longer ones leave fewer parts to join
+  p.chunk_tokens = T >= 65536 ? 64 : T >= 8192 ? 32 : 16;
+  p.chunks = (T + p.chunk_tokens - 1) / p.chunk_tokens;
   p.cnt = 0;
   p.below = p.cnt + up(p.segs * p.ranges * kRange * 4);
   p.start = p.below + up(p.segs * p.ranges * 4);
@@ -402,27 +508,32 @@ hipError_t launch_bwd(const Id* ids, int64_t T, const _Float16* dout, int64_t V,
   int2* sorted = reinterpret_cast<int2*>(ws + p.sorted);
   float* parts = reinterpret_cast<float*>(ws + p.parts);
   const dim3 grid((unsigned)p.ranges, (unsigned)p.segs);
-  hipLaunchKernelGGL((embed_count_kernel<Id>), grid, dim3(kRange), 0, s, ids, T, V, p.seg_tokens, cnt, below);
-  hipLaunchKernelGGL((embed_place_kernel<Id>), grid, dim3(kRange), 0, s, ids, T, V, p.seg_tokens, cnt, below, start,
-                     sorted);
-  if (T > 0) {
-    const int vec = d % 8 == 0 ? 8 : 1;
-    int team = 8;
-    while (team < kThreads && team * vec < d) team *= 2;
-    const dim3 sums((unsigned)((p.chunks + kThreads / team - 1) / (kThreads / team)),
-                    (unsigned)((d + team * vec - 1) / (team * vec)));
-    if (vec == 8)
-      hipLaunchKernelGGL((embed_sum_kernel<8>), sums, dim3(kThreads), 0, s, sorted, start, dout, V, d, scale, team,
-                         (int)add, parts, dtable);
-    else
-      hipLaunchKernelGGL((embed_sum_kernel<1>), sums, dim3(kThreads), 0, s, sorted, start, dout, V, d, scale, team,
-                         (int)add, parts, dtable);
-    hipLaunchKernelGGL(embed_join_kernel, dim3((unsigned)p.chunks), dim3(kThreads), 0, s, sorted, start, V, d, scale,
-                       (int)add, parts, dtable);
+  if (T <= kSelfCount) {
+    hipLaunchKernelGGL((embed_place_kernel<Id, true>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, nullptr, nullptr,
+                       start, sorted);
+  } else {
+    hipLaunchKernelGGL((embed_count_kernel<Id>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below);
+    hipLaunchKernelGGL((embed_place_kernel<Id, false>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below, start,
+                       sorted);
   }
-  if (!add)
-    hipLaunchKernelGGL(embed_clear_kernel, dim3((unsigned)((V + kClearRows - 1) / kClearRows)), dim3(kThreads), 0, s,
-                       start, V, d, dtable);
+  const int vec = d % 8 == 0 ? 8 : 1;
+  int team = 8;
+  while (team < kThreads && team * vec < d) team *= 2;
+  const int sum_blocks = (int)((p.chunks + kThreads / team - 1) / (kThreads / team));
+  const int64_t clear_blocks = add ? 0 : (V + kClearRows - 1) / kClearRows;
+  const dim3 sums((unsigned)(sum_blocks + clear_blocks), (unsigned)((d + team * vec - 1) / (team * vec)));
+  const int chunk = (int)p.chunk_tokens;
+  auto sum = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, sums, dim3(kThreads), 0, s, sorted, start, dout, V, d, scale, team, chunk, sum_blocks, parts,
+                       dtable);
+  };
+  if (vec == 8)
+    add ? sum(embed_sum_kernel<8, true>) : sum(embed_sum_kernel<8, false>);
+  else
+    add ? sum(embed_sum_kernel<1, true>) : sum(embed_sum_kernel<1, false>);
+  if (p.chunks > 1)
+    hipLaunchKernelGGL(embed_join_kernel, dim3((unsigned)(p.chunks - 1), (unsigned)((d + 255) / 256)), dim3(64 * kJoinWaves),
+                       0, s, sorted, start, V, d, scale, chunk, (int)add, parts, dtable);
   return hipGetLastError();
 }
 
