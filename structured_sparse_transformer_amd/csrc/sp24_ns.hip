@@ -760,6 +760,241 @@ __global__ __launch_bounds__(64 * T::WAVES) void ns_join_kernel(Jobs jobs, Step 
                              tn * T::BN + wave / T::WAVES_M * T::WN + t * 32, acc[0], acc[1], smem + wave * (32 * kTurn), lane);
 }
 
+// All of a small weight's steps in one workgroup, with X, A and B in LDS, in the
+// blocks and swizzle that a stage of the large products has there.  A chain of
+// launches takes 4 us a product whatever its size; 64 x 64 and five steps took
+// 76 us of them.  Every product's tiles are made with the operands such that a
+// lane ends up with four neighbours of a row of the result: of A and B, which
+// are symmetric, both halves are computed; of X, a wave makes whole columns of
+// blocks, which nothing else reads, and puts them back in place.
+constexpr int kSmallThreads = 512, kSmallBytes = 152 * 1024, kSmallRows = 4;   // blocks of 32
+struct Coefs {
+  float c[3 * kMaxNsSteps];
+};
+
+template <bool SPLIT>
+constexpr int64_t small_bytes(int64_t na, int64_t nx) {
+  return 2048 * (2 * na * nx + (SPLIT ? 4 : 2) * na * na);
+}
+
+template <bool SPLIT>
+__global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coefs coefs, int steps, float mu, bool nesterov,
+                                                                  float eps) {
+  constexpr int PARTS = SPLIT ? 2 : 1, WAVES = kSmallThreads / 64;
+  __shared__ __align__(1024) unsigned char smem[kSmallBytes];
+  __shared__ double wave_sums[WAVES];
+  const Job& j = jobs.j[blockIdx.x];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 5, l32 = lane & 31, na = j.na, nx = j.nx;
+  const int xplane = na * nx * 2048, aplane = na * na * 2048;
+  const int X = 0, A = 2 * xplane, B = A + PARTS * aplane;   // byte offsets
+
+  // momentum and norm
+  const int64_t total = (int64_t)j.m * j.n;
+  double sum = 0.0;
+  for (int64_t i = tid * 8; i < total; i += kSmallThreads * 8) {
+    float u[8];
+    load8(j.G, j.g32, i, total, u);
+    if (j.M != nullptr) {
+      float m[8];
+      load8(j.M, true, i, total, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        m[e] = mu * m[e] + u[e];
+        u[e] = nesterov ? u[e] + mu * m[e] : m[e];
+      }
+      store8(j.M, i, total, m);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)u[e] * (double)u[e];
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) wave_sums[wave] = sum;
+  __syncthreads();   // and the new momentum is there for all
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) sum += wave_sums[w];
+  const double scale = (double)kScale / (sqrt(sum) + (double)eps);
+
+  // X_0: a chunk of eight of a row at a time; zeros past m and n
+  for (int k = tid; k < na * nx * 128; k += kSmallThreads) {
+    const int blk = k / 128, r = k / 4 % 32, q = k % 4, row = blk / nx * 32 + r, col = blk % nx * 32 + q * 8;
+    float u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool in = row < j.m && col + e < j.n;
+      const int64_t i = !in ? 0 : j.tall ? (int64_t)(col + e) * j.m + row : (int64_t)row * j.n + col + e;
+      const float v = update_of(j, i, mu, nesterov);
+      u[e] = in ? (float)((double)v * scale) : 0.0f;
+    }
+    _Float16* const to = reinterpret_cast<_Float16*>(smem + X + blk * 2048 + r * 64 + (q ^ (r >> 2 & 3)) * 16);
+    put8(to, xplane / 2, true, u);
+  }
+  __syncthreads();
+
+  const int swz = l32 >> 2 & 3;
+  const int G = lane >> 4, j4 = (lane & 15) >> 2, c4 = lane & 3;
+  const int tr_q = 2 * (G & 1) + (c4 >> 1), tr_row = (8 * (G >> 1) + j4) * 64 + (c4 & 1) * 8;
+  const int tr_lo = tr_row + (tr_q ^ (2 * (G >> 1))) * 16, tr_hi = tr_row + (tr_q ^ (2 * (G >> 1) + 1)) * 16 + 4 * 64;
+  auto row_frag = [&](int block, int ks) __attribute__((always_inline)) {
+    return *reinterpret_cast<const h8*>(smem + block + l32 * 64 + (((2 * ks + g) ^ swz) * 16));
+  };
+  auto tr_frag = [&](int block, int ks) __attribute__((always_inline)) {
+    const int o = block + ks * 16 * 64;
+    const h4 lo = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)((lds_u8*)smem + o + tr_lo)));
+    const h4 hi = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)((lds_u8*)smem + o + tr_hi)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto mfma = [&](f16v& acc, const h8 (&l)[PARTS], const h8 (&r)[PARTS]) __attribute__((always_inline)) {
+    if constexpr (SPLIT) {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[0], r[1], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[1], r[0], acc, 0, 0, 0);
+    }
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(l[0], r[0], acc, 0, 0, 0);
+  };
+  // this lane's four values 4 q .. 4 q + 3 of a tile: row l32, columns 8 q + 4 g ..
+  auto four = [&](int block, int q) __attribute__((always_inline)) { return block + l32 * 64 + (q ^ swz) * 16 + g * 8; };
+  auto get4 = [&](int at, int plane, bool both, float (&v)[4]) __attribute__((always_inline)) {
+    const h4 hi = *reinterpret_cast<const h4*>(smem + at);
+    const h4 lo = both ? *reinterpret_cast<const h4*>(smem + at + plane) : h4{};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)hi[e] + (float)lo[e];
+  };
+  auto put4 = [&](int at, int plane, bool both, const float (&v)[4]) __attribute__((always_inline)) {
+    h4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      _Float16 h, l;
+      split(v[e], h, l);
+      hi[e] = h;
+      lo[e] = l;
+    }
+    *reinterpret_cast<h4*>(smem + at) = hi;
+    if (both) *reinterpret_cast<h4*>(smem + at + plane) = lo;
+  };
+  auto zero = [](f16v& acc) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  };
+
+  for (int k = 0; k < steps; ++k) {
+    const float a = coefs.c[3 * k], b = coefs.c[3 * k + 1], c = coefs.c[3 * k + 2];
+    const bool in_q = SPLIT || k >= kLoSteps, last = k + 1 == steps;
+    // A = X X^T, then B = b A + c A A (+ a I); tile (t / na, t % na) is stored transposed
+    for (int t = wave; t < na * na; t += WAVES) {
+      const int ti = t / na, tj = t % na;
+      f16v acc;
+      zero(acc);
+      for (int kb = 0; kb < nx; ++kb)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          h8 l[PARTS], r[PARTS];
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            l[p] = row_frag(X + p * xplane + (ti * nx + kb) * 2048, ks);
+            r[p] = row_frag(X + p * xplane + (tj * nx + kb) * 2048, ks);
+          }
+          mfma(acc, l, r);
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[4 * q + e] * kInvScale;
+        put4(four(A + (tj * na + ti) * 2048, q), aplane, SPLIT, v);
+      }
+    }
+    __syncthreads();
+    for (int t = wave; t < na * na; t += WAVES) {
+      const int ti = t / na, tj = t % na;
+      f16v acc;
+      zero(acc);
+      for (int kb = 0; kb < na; ++kb)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          h8 l[PARTS], r[PARTS];
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            l[p] = row_frag(A + p * aplane + (ti * na + kb) * 2048, ks);
+            r[p] = row_frag(A + p * aplane + (tj * na + kb) * 2048, ks);
+          }
+          mfma(acc, l, r);
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4], was[4];
+        get4(four(A + (tj * na + ti) * 2048, q), aplane, SPLIT, was);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = b * was[e] + c * (acc[4 * q + e] * kInvScale);
+          if (in_q && ti == tj && l32 == 8 * q + 4 * g + e) v[e] += a * kScale;
+        }
+        put4(four(B + (tj * na + ti) * 2048, q), aplane, SPLIT, v);
+      }
+    }
+    __syncthreads();
+    // X <- a X + B X, or B X: transposed, X^T B, so that a lane has four columns of a row
+    for (int t = wave; t < nx; t += WAVES) {
+      f16v acc[kSmallRows];
+#pragma unroll
+      for (int i = 0; i < kSmallRows; ++i) {
+        zero(acc[i]);
+        if (i >= na) continue;
+        for (int kb = 0; kb < na; ++kb)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            h8 l[PARTS], r[PARTS];
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+              l[p] = tr_frag(X + p * xplane + (kb * nx + t) * 2048, ks);
+              r[p] = row_frag(B + p * aplane + (i * na + kb) * 2048, ks);
+            }
+            mfma(acc[i], l, r);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < kSmallRows; ++i) {
+        if (i >= na) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int at = four(X + (i * nx + t) * 2048, q);
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][4 * q + e] * kInvScale;
+          if (!in_q) {
+            float was[4];
+            get4(at, xplane, true, was);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += a * was[e];
+          }
+          if (!last) {
+            put4(at, xplane, true, v);
+            continue;
+          }
+          const int row = i * 32 + l32, col = t * 32 + 8 * q + 4 * g;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (row >= j.m || col + e >= j.n) continue;
+            const float x = v[e] * kInvScale;
+            const int64_t o = j.tall ? (int64_t)(col + e) * j.m + row : (int64_t)row * j.n + col + e;
+            if (j.P != nullptr) {
+              const float p = j.keep * j.P[o] - j.lr * x;
+              j.P[o] = p;
+              if (j.W != nullptr) j.W[o] = __builtin_bit_cast(uint16_t, (_Float16)p);
+            } else if (j.out32) {
+              static_cast<float*>(j.out)[o] = x;
+            } else {
+              static_cast<_Float16*>(j.out)[o] = (_Float16)x;
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The tiles.  Square, for A and for all last products too small for the others:
@@ -800,14 +1035,20 @@ int64_t lay_out(Job& j, unsigned char* base) {
   return at;
 }
 
-int64_t fill(Jobs& jobs, const NsJob* in, int count, bool split, unsigned char* ws) {
-  int64_t at = 0;
-  jobs.count = 0;
+template <bool SPLIT>
+bool is_small(const Job& j) {
+  return j.na <= kSmallRows && small_bytes<SPLIT>(j.na, j.nx) <= kSmallBytes;
+}
+
+// The launch's weights, small ones apart; returns the workspace's bytes, which
+// do not depend on `split`.
+int64_t fill(Jobs& large, Jobs& small, const NsJob* in, int count, bool split, unsigned char* ws) {
+  int64_t at = 0, tiles = 0;
+  Jobs all{};
   for (int k = 0; k < count; ++k) {
     const NsJob& s = in[k];
     if (s.R == 0 || s.C == 0) continue;
-    Job& j = jobs.j[jobs.count++];
-    j = Job{};
+    Job& j = all.j[all.count++];
     j.G = s.G;
     j.M = s.M;
     j.out = s.out;
@@ -824,13 +1065,20 @@ int64_t fill(Jobs& jobs, const NsJob* in, int count, bool split, unsigned char* 
     j.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
     j.g32 = s.g32;
     j.out32 = s.out32;
+    if (!is_small<true>(j)) tiles += upper_tiles<Square<false>>(j.m);
   }
-  int64_t tiles = 0;
-  for (int k = 0; k < jobs.count; ++k) tiles += upper_tiles<Square<false>>(jobs.j[k].m);
-  for (int k = 0; k < jobs.count; ++k) {
-    Job& j = jobs.j[k];
-    j.gram_splits = splits_for(tiles, split ? 1 : 2, 32 * j.nx);
+  for (int k = 0; k < all.count; ++k) {
+    Job& j = all.j[k];
+    if (is_small<true>(j)) {
+      at += 256;   // so that every call has a workspace
+      small.j[small.count++] = j;
+      continue;
+    }
+    j.gram_splits = splits_for(tiles, 2, 32 * j.nx);
     at += lay_out(j, ws ? ws + at : nullptr);
+    if (split) j.gram_splits = splits_for(tiles, 1, 32 * j.nx);
+    Jobs& to = !split && is_small<false>(j) ? small : large;
+    to.j[to.count++] = j;
   }
   return at;
 }
@@ -916,14 +1164,21 @@ void step(Jobs& jobs, const NsParams& prm, int k, hipStream_t s) {
 }  // namespace
 
 int64_t ns_workspace(const NsJob* jobs, int count) {
-  Jobs j{};
-  return fill(j, jobs, count, false, nullptr);
+  Jobs large{}, small{};
+  return fill(large, small, jobs, count, false, nullptr);
 }
 
 hipError_t launch_newton_schulz(const NsJob* in, int count, const NsParams& prm, void* ws, hipStream_t s) {
-  Jobs jobs{};
-  fill(jobs, in, count, prm.split, static_cast<unsigned char*>(ws));
-  if (jobs.count == 0) return hipSuccess;
+  Jobs jobs{}, small{};
+  fill(jobs, small, in, count, prm.split, static_cast<unsigned char*>(ws));
+  if (small.count > 0) {
+    Coefs c{};
+    for (int k = 0; k < 3 * prm.steps; ++k) c.c[k] = prm.coef[k];
+    const auto kernel = prm.split ? ns_small_kernel<true> : ns_small_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)small.count), dim3(kSmallThreads), 0, s, small, c, prm.steps, prm.mu,
+                       prm.nesterov, prm.eps);
+  }
+  if (jobs.count == 0) return hipGetLastError();
   const unsigned norm = deal(jobs, [](const Job& j) { return (int64_t)j.parts; });
   hipLaunchKernelGGL(ns_norm_kernel, dim3(norm), dim3(kThreads), 0, s, jobs, prm.mu, prm.nesterov);
   const unsigned start = deal(jobs, [](const Job& j) { return (int64_t)j.na * ((j.nx + 1) / 2); });
