@@ -83,6 +83,7 @@ struct Job {
 struct Jobs {
   Job j[kMaxNsJobs];
   int count;
+  bool fine;   // few tiles: small ones throughout
 };
 
 __device__ __forceinline__ const Job& job_of(const Jobs& jobs, int block) {
@@ -392,7 +393,14 @@ __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror
       const int col = j.tall ? r0 + (lane & 3) * 8 : c0 + ec;
       o[p] = (int64_t)row * width + col;
       left[p] = row < (j.tall ? j.n : j.m) ? min(8, width - col) : 0;
-      if (whole && j.P != nullptr && left[p] > 0) load8(j.P, true, o[p], o[p] + 8, pw[p]);
+      if (j.P != nullptr && left[p] > 0) {
+        if (whole) {
+          load8(j.P, true, o[p], o[p] + 8, pw[p]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pw[p][e] = j.P[o[p] + min(e, left[p] - 1)];
+        }
+      }
     }
   }
 #pragma unroll
@@ -437,7 +445,7 @@ __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror
         for (int e = 0; e < 8; ++e) v[e] = from[e * step];
         const int row = c0 + p * 16 + (lane >> 2), col = r0 + (lane & 3) * 8;
         if (row < 32 * j.na && col < 32 * j.na) put8(D + at_block(row, col, nb), plane, SPLIT, v);
-      } else if (whole) {
+      } else {
         if (left[p] <= 0) continue;
         float v[8];
 #pragma unroll
@@ -445,29 +453,23 @@ __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror
         if (j.P != nullptr) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = j.keep * pw[p][e] - j.lr * v[e];
-          store8(j.P, o[p], o[p] + 8, v);
         }
-        if (j.P == nullptr && j.out32) {
-          store8(static_cast<float*>(j.out), o[p], o[p] + 8, v);
-        } else if (j.P == nullptr || j.W != nullptr) {
-          h8 h;
+        float* const to32 = j.P != nullptr ? j.P : j.out32 ? static_cast<float*>(j.out) : nullptr;
+        _Float16* const to16 = j.P != nullptr ? reinterpret_cast<_Float16*>(j.W) : j.out32 ? nullptr : static_cast<_Float16*>(j.out);
+        if (whole) {
+          if (to32 != nullptr) store8(to32, o[p], o[p] + 8, v);
+          if (to16 != nullptr) {
+            h8 h;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
-          *reinterpret_cast<h8*>((j.P != nullptr ? reinterpret_cast<_Float16*>(j.W) : static_cast<_Float16*>(j.out)) + o[p]) = h;
-        }
-      } else {
-#pragma unroll 1
-        for (int e = 0; e < left[p]; ++e) {
-          float v = from[e * step];
-          const int64_t i = o[p] + e;
-          if (j.P != nullptr) {
-            v = j.keep * j.P[i] - j.lr * v;
-            j.P[i] = v;
-            if (j.W != nullptr) j.W[i] = __builtin_bit_cast(uint16_t, (_Float16)v);
-          } else if (j.out32) {
-            static_cast<float*>(j.out)[i] = v;
-          } else {
-            static_cast<_Float16*>(j.out)[i] = (_Float16)v;
+            for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
+            *reinterpret_cast<h8*>(to16 + o[p]) = h;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e >= left[p]) continue;
+            if (to32 != nullptr) to32[o[p] + e] = v[e];
+            if (to16 != nullptr) to16[o[p] + e] = (_Float16)v[e];
           }
         }
       }
@@ -789,10 +791,10 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
   const int xplane = na * nx * 2048, aplane = na * na * 2048;
   const int X = 0, A = 2 * xplane, B = A + PARTS * aplane;   // byte offsets
 
-  // momentum and norm
-  const int64_t total = (int64_t)j.m * j.n;
+  // momentum and norm, eight entries of U at a time
+  const int total = j.m * j.n, width = j.tall ? j.m : j.n;
   double sum = 0.0;
-  for (int64_t i = tid * 8; i < total; i += kSmallThreads * 8) {
+  for (int i = tid * 8; i < total; i += kSmallThreads * 8) {
     float u[8];
     load8(j.G, j.g32, i, total, u);
     if (j.M != nullptr) {
@@ -811,25 +813,55 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
   if (lane == 0) wave_sums[wave] = sum;
-  __syncthreads();   // and the new momentum is there for all
+  for (int i = tid; i < 2 * xplane / 16; i += kSmallThreads) reinterpret_cast<i32x4*>(smem + X)[i] = i32x4{};
+  __syncthreads();
   sum = 0.0;
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) sum += wave_sums[w];
   const double scale = (double)kScale / (sqrt(sum) + (double)eps);
 
-  // X_0: a chunk of eight of a row at a time; zeros past m and n
-  for (int k = tid; k < na * nx * 128; k += kSmallThreads) {
-    const int blk = k / 128, r = k / 4 % 32, q = k % 4, row = blk / nx * 32 + r, col = blk % nx * 32 + q * 8;
-    float u[8];
+  // Where X has U's entries i .. i + 7: in one 16-byte piece if U's rows are X's
+  // and hold whole eights, else each for itself.
+  const bool pieces = !j.tall && width % 8 == 0;
+  const auto place = [&](int row, int col) __attribute__((always_inline)) {
+    return X + ((row >> 5) * nx + (col >> 5)) * 2048 + (row & 31) * 64 + ((col >> 3 & 3) ^ (row >> 2 & 3)) * 16 + (col & 7) * 2;
+  };
+  const auto places = [&](int i, int (&at)[8]) __attribute__((always_inline)) {
+    int r = i / width, k = i - r * width;   // of U
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const bool in = row < j.m && col + e < j.n;
-      const int64_t i = !in ? 0 : j.tall ? (int64_t)(col + e) * j.m + row : (int64_t)row * j.n + col + e;
-      const float v = update_of(j, i, mu, nesterov);
-      u[e] = in ? (float)((double)v * scale) : 0.0f;
+      at[e] = j.tall ? place(k, r) : place(r, k);
+      if (++k == width) {
+        k = 0;
+        ++r;
+      }
     }
-    _Float16* const to = reinterpret_cast<_Float16*>(smem + X + blk * 2048 + r * 64 + (q ^ (r >> 2 & 3)) * 16);
-    put8(to, xplane / 2, true, u);
+  };
+  for (int i = tid * 8; i < total; i += kSmallThreads * 8) {
+    float u[8];
+    load8(j.G, j.g32, i, total, u);
+    if (j.M != nullptr) {
+      float m[8];   // this thread's own stores
+      load8(j.M, true, i, total, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = nesterov ? u[e] + mu * m[e] : m[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = (float)((double)u[e] * scale);
+    int at[8];
+    places(i, at);
+    if (pieces) {
+      put8(reinterpret_cast<_Float16*>(smem + at[0]), xplane / 2, true, u);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (i + e >= total) continue;
+        _Float16 hi, lo;
+        split(u[e], hi, lo);
+        *reinterpret_cast<_Float16*>(smem + at[e]) = hi;
+        *reinterpret_cast<_Float16*>(smem + at[e] + xplane) = lo;
+      }
+    }
   }
   __syncthreads();
 
@@ -880,7 +912,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
 
   for (int k = 0; k < steps; ++k) {
     const float a = coefs.c[3 * k], b = coefs.c[3 * k + 1], c = coefs.c[3 * k + 2];
-    const bool in_q = SPLIT || k >= kLoSteps, last = k + 1 == steps;
+    const bool in_q = SPLIT || k >= kLoSteps;
     // A = X X^T, then B = b A + c A A (+ a I); tile (t / na, t % na) is stored transposed
     for (int t = wave; t < na * na; t += WAVES) {
       const int ti = t / na, tj = t % na;
@@ -968,30 +1000,50 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += a * was[e];
           }
-          if (!last) {
-            put4(at, xplane, true, v);
-            continue;
-          }
-          const int row = i * 32 + l32, col = t * 32 + 8 * q + 4 * g;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (row >= j.m || col + e >= j.n) continue;
-            const float x = v[e] * kInvScale;
-            const int64_t o = j.tall ? (int64_t)(col + e) * j.m + row : (int64_t)row * j.n + col + e;
-            if (j.P != nullptr) {
-              const float p = j.keep * j.P[o] - j.lr * x;
-              j.P[o] = p;
-              if (j.W != nullptr) j.W[o] = __builtin_bit_cast(uint16_t, (_Float16)p);
-            } else if (j.out32) {
-              static_cast<float*>(j.out)[o] = x;
-            } else {
-              static_cast<_Float16*>(j.out)[o] = (_Float16)x;
-            }
-          }
+          put4(at, xplane, true, v);
         }
       }
     }
     __syncthreads();
+  }
+
+  // the outcome, in U's order; both parts of X are 22 bits of it
+  for (int i = tid * 8; i < total; i += kSmallThreads * 8) {
+    float p[8], x[8];
+    if (j.P != nullptr) load8(j.P, true, i, total, p);
+    int at[8];
+    places(i, at);
+    h8 hi, lo;
+    if (pieces) {
+      hi = *reinterpret_cast<const h8*>(smem + at[0]);
+      lo = *reinterpret_cast<const h8*>(smem + at[0] + xplane);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = i + e < total ? at[e] : at[0];
+        hi[e] = *reinterpret_cast<const _Float16*>(smem + k);
+        lo[e] = *reinterpret_cast<const _Float16*>(smem + k + xplane);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = ((float)hi[e] + (float)lo[e]) * kInvScale;
+      if (j.P != nullptr) x[e] = j.keep * p[e] - j.lr * x[e];
+    }
+    if (j.P != nullptr || j.out32) store8(j.P != nullptr ? j.P : static_cast<float*>(j.out), i, total, x);
+    if (j.P != nullptr ? j.W != nullptr : !j.out32) {
+      _Float16* const to = (j.P != nullptr ? reinterpret_cast<_Float16*>(j.W) : static_cast<_Float16*>(j.out)) + i;
+      h8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = (_Float16)x[e];
+      if (i + 8 <= total) {
+        *reinterpret_cast<h8*>(to) = h;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i + e < total) to[e] = h[e];
+      }
+    }
   }
 }
 
@@ -1016,8 +1068,13 @@ int splits_for(int64_t tiles, int per_cu, int K) {
   return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 
+template <class T>
+int64_t partial_bytes(const Job& j) {
+  return upper_tiles<T>(j.m) * j.gram_splits * T::BM * T::BN * 4;
+}
+
 // Bytes of one weight's workspace; fills its pointers when base is given.
-int64_t lay_out(Job& j, unsigned char* base) {
+int64_t lay_out(Job& j, bool fine, unsigned char* base) {
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     unsigned char* p = base ? base + at : nullptr;
@@ -1031,7 +1088,9 @@ int64_t lay_out(Job& j, unsigned char* base) {
   j.A = reinterpret_cast<_Float16*>(take(a));
   j.B = reinterpret_cast<_Float16*>(take(a));
   const int splits = j.gram_splits;
-  j.partial = reinterpret_cast<float*>(take(splits > 1 ? upper_tiles<Square<false>>(j.m) * splits * Square<false>::BM * Square<false>::BN * 4 : 0));
+  j.partial = reinterpret_cast<float*>(take(splits <= 1 ? 0
+                                                : fine    ? partial_bytes<Small<false>>(j)
+                                                          : partial_bytes<Square<false>>(j)));
   return at;
 }
 
@@ -1043,7 +1102,7 @@ bool is_small(const Job& j) {
 // The launch's weights, small ones apart; returns the workspace's bytes, which
 // do not depend on `split`.
 int64_t fill(Jobs& large, Jobs& small, const NsJob* in, int count, bool split, unsigned char* ws) {
-  int64_t at = 0, tiles = 0;
+  int64_t at = 0, squares = 0, upper = 0, upper_fine = 0;
   Jobs all{};
   for (int k = 0; k < count; ++k) {
     const NsJob& s = in[k];
@@ -1065,8 +1124,13 @@ int64_t fill(Jobs& large, Jobs& small, const NsJob* in, int count, bool split, u
     j.parts = (int)(parts < kMaxParts ? parts : kMaxParts);
     j.g32 = s.g32;
     j.out32 = s.out32;
-    if (!is_small<true>(j)) tiles += upper_tiles<Square<false>>(j.m);
+    if (is_small<true>(j)) continue;
+    squares += up(j.m, Square<false>::BM) / Square<false>::BM * (up(j.n, Square<false>::BN) / Square<false>::BN);
+    upper += upper_tiles<Square<false>>(j.m);
+    upper_fine += upper_tiles<Small<false>>(j.m);
   }
+  // where even twice the tiles leave CUs idle, tiles half as large
+  large.fine = 2 * squares <= device_cu_count();
   for (int k = 0; k < all.count; ++k) {
     Job& j = all.j[k];
     if (is_small<true>(j)) {
@@ -1074,8 +1138,9 @@ int64_t fill(Jobs& large, Jobs& small, const NsJob* in, int count, bool split, u
       small.j[small.count++] = j;
       continue;
     }
+    const int64_t tiles = large.fine ? upper_fine : upper;
     j.gram_splits = splits_for(tiles, 2, 32 * j.nx);
-    at += lay_out(j, ws ? ws + at : nullptr);
+    at += lay_out(j, large.fine, ws ? ws + at : nullptr);
     if (split) j.gram_splits = splits_for(tiles, 1, 32 * j.nx);
     Jobs& to = !split && is_small<false>(j) ? small : large;
     to.j[to.count++] = j;
@@ -1135,7 +1200,10 @@ template <bool SPLIT>
 void step(Jobs& jobs, const NsParams& prm, int k, hipStream_t s) {
   const Step st{k & 1, prm.coef[3 * k], prm.coef[3 * k + 1], prm.coef[3 * k + 2], SPLIT || k >= kLoSteps,
                 SPLIT || k + 1 < kLoSteps};
-  product<kGram, SPLIT, false, false, Square<SPLIT>>(jobs, st, s);
+  if (jobs.fine)
+    product<kGram, SPLIT, false, false, Small<SPLIT>>(jobs, st, s);
+  else
+    product<kGram, SPLIT, false, false, Square<SPLIT>>(jobs, st, s);
   product<kPoly, SPLIT, false, false, Small<SPLIT>>(jobs, st, s);
   const bool last = k + 1 == prm.steps;
   // The larger tile where its whole rounds over the CUs cost less, by area over
@@ -1144,6 +1212,10 @@ void step(Jobs& jobs, const NsParams& prm, int k, hipStream_t s) {
   // squares, three to a CU, are taken to fill the CUs evenly).  Split ones: 1024
   // x 4096 and its transpose take 51 us in 256 Broad tiles, 59 us in 512 Square
   // ones.
+  if (jobs.fine) {
+    apply<SPLIT, Small<SPLIT>>(jobs, st, last, s);
+    return;
+  }
   const int64_t cus = device_cu_count();
   const int64_t squares = apply_tiles<Square<SPLIT>>(jobs);
   if constexpr (SPLIT) {
