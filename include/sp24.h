@@ -435,13 +435,12 @@ enum {
  *
  *   ids     in   [T], SP24_I32 or SP24_I64 (id_type)
  *   table   in   [V, d], SP24_F16 or SP24_F32 (table_type)
- *   T, V, d      >= 0, of any size (widths that are multiples of 8 are read
- *                16 bytes at a time)
+ *   T, V, d      >= 0, of any size
  *   out     out  fp16 [T, d] (may not overlap the table)
  * Errors: NULL (the table may be NULL when V is 0), SHAPE, ALIGN, LAUNCH;
  * UNSUPPORTED for another type; TOO_LARGE when T, V or d reaches 2^31, a
- * matrix 2^40 entries, or the output 2^34 chunks of 8 entries (of 1 entry
- * where d is not a multiple of 8).
+ * matrix 2^40 entries, or the output about 2^34 chunks of 8 entries of a row
+ * (of 1 entry where d is below 8).
  */
 int sp24_embed_fwd(const void* ids, int id_type, int64_t T, const void* table, int table_type, int64_t V, int64_t d,
                    float scale, void* out, void* stream);

@@ -311,7 +311,7 @@ int sp24_embed_fwd(const void* ids, int id_type, int64_t T, const void* table, i
   if (st != SP24_OK) return st;
   if ((st = check_dims(V, d, 1)) != SP24_OK) return st;
   // a work-item takes four chunks of 8 entries, or of 1
-  if (T != 0 && (d % 8 == 0 ? d / 8 : d) > 4 * (kMaxLaunchItems - 256) / T) return SP24_ERR_TOO_LARGE;
+  if (T != 0 && (d >= 8 ? (d + 7) / 8 : d) > 4 * (kMaxLaunchItems - 256) / T) return SP24_ERR_TOO_LARGE;
   if (T == 0 || d == 0) return SP24_OK;
   if (ids == nullptr || out == nullptr || (V != 0 && table == nullptr)) return SP24_ERR_NULL;
   if (!aligned16(ids) || !aligned16(out) || (V != 0 && !aligned16(table))) return SP24_ERR_ALIGN;

@@ -21,6 +21,13 @@ namespace {
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
+// Rows of any width are read and written 16 bytes at a time: the hardware takes
+// such accesses at the element's alignment.  The last piece of a row begins at
+// d - 8, over a part of the one before, whose values it has too; rows narrower
+// than 8 go an element at a time.
+typedef h8 h8u __attribute__((aligned(2)));
+typedef f4 f4u __attribute__((aligned(4)));
+
 constexpr int kThreads = 256;
 constexpr int kItems = 4;   // row chunks per thread of the forward: that many gathers in flight
 
@@ -28,13 +35,13 @@ template <typename T>
 __device__ __forceinline__ void load_row8(const T* p, float (&v)[8]);
 template <>
 __device__ __forceinline__ void load_row8<_Float16>(const _Float16* p, float (&v)[8]) {
-  const h8 x = *reinterpret_cast<const h8*>(p);
+  const h8 x = *reinterpret_cast<const h8u*>(p);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = (float)x[e];
 }
 template <>
 __device__ __forceinline__ void load_row8<float>(const float* p, float (&v)[8]) {
-  const f4 x = *reinterpret_cast<const f4*>(p), y = *reinterpret_cast<const f4*>(p + 4);
+  const f4 x = *reinterpret_cast<const f4u*>(p), y = *reinterpret_cast<const f4u*>(p + 4);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     v[e] = x[e];
@@ -42,25 +49,25 @@ __device__ __forceinline__ void load_row8<float>(const float* p, float (&v)[8]) 
   }
 }
 
-// A row is d / VEC chunks; a workgroup takes kThreads * kItems consecutive
-// chunks of the flattened [T, d / VEC] output.
+// A row is d / VEC chunks, rounded up; a workgroup takes kThreads * kItems
+// consecutive chunks of all rows'.
 template <typename Table, typename Id, int VEC>
 __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(const Id* __restrict__ ids, const Table* __restrict__ table,
                                                               int64_t T, int64_t V, int64_t d, float scale,
                                                               _Float16* __restrict__ out) {
-  const uint32_t chunks = (uint32_t)(d / VEC);
+  const uint32_t chunks = (uint32_t)((d + VEC - 1) / VEC);
   const int64_t first = (int64_t)blockIdx.x * (kThreads * kItems);
   const int64_t t0 = first / chunks;
   const uint32_t c0 = (uint32_t)(first - t0 * chunks);
   // no branches around the loads: kItems gathers are in flight
   int64_t t[kItems], id[kItems];
-  uint32_t c[kItems];
+  int64_t c[kItems];   // first column
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const uint32_t i = c0 + threadIdx.x + k * kThreads;   // c0 < chunks <= 2^31
     const uint32_t q = i / chunks;
     t[k] = t0 + q;
-    c[k] = i - q * chunks;
+    c[k] = min<int64_t>((int64_t)(i - q * chunks) * VEC, d - VEC);
     id[k] = (int64_t)ids[min<int64_t>(t[k], T - 1)];
   }
   float v[kItems][VEC];
@@ -72,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(const Id* __restric
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
       const int64_t r = id[k] >= 0 && id[k] < V ? id[k] : 0;
-      const Table* row = table + r * d + (int64_t)c[k] * VEC;
+      const Table* row = table + r * d + c[k];
       if constexpr (VEC == 8)
         load_row8<Table>(row, v[k]);
       else
@@ -86,12 +93,12 @@ __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(const Id* __restric
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     if (t[k] >= T) continue;
-    _Float16* o = out + t[k] * d + (int64_t)c[k] * VEC;
+    _Float16* o = out + t[k] * d + c[k];
     if constexpr (VEC == 8) {
       h8 h;
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[k][e];
-      *reinterpret_cast<h8*>(o) = h;
+      *reinterpret_cast<h8u*>(o) = h;
     } else {
       o[0] = (_Float16)v[k][0];
     }
@@ -104,8 +111,8 @@ hipError_t launch_fwd(const void* ids, const void* table, int64_t T, int64_t V, 
   const Id* i = static_cast<const Id*>(ids);
   const Table* tb = static_cast<const Table*>(table);
   _Float16* o = reinterpret_cast<_Float16*>(out);
-  const int vec = d % 8 == 0 ? 8 : 1;   // rows of other widths are not 16-byte aligned
-  const int64_t items = T * (d / vec);
+  const int vec = d >= 8 ? 8 : 1;
+  const int64_t items = T * ((d + vec - 1) / vec);
   const dim3 grid((unsigned)((items + kThreads * kItems - 1) / (kThreads * kItems)));
   if (vec == 8)
     hipLaunchKernelGGL((embed_fwd_kernel<Table, Id, 8>), grid, dim3(kThreads), 0, s, i, tb, T, V, d, scale, o);
@@ -316,7 +323,7 @@ struct Row;
 template <>
 struct Row<8> {
   h8 x;
-  __device__ __forceinline__ void load(const _Float16* p) { x = __builtin_nontemporal_load(reinterpret_cast<const h8*>(p)); }
+  __device__ __forceinline__ void load(const _Float16* p) { x = __builtin_nontemporal_load(reinterpret_cast<const h8u*>(p)); }
   __device__ __forceinline__ float at(int e) const { return (float)x[e]; }
 };
 template <>
@@ -330,7 +337,7 @@ struct Row<1> {
 template <int VEC>
 __device__ __forceinline__ void load_sum(const float* p, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
-    const f4 x = *reinterpret_cast<const f4*>(p), y = *reinterpret_cast<const f4*>(p + 4);
+    const f4 x = *reinterpret_cast<const f4u*>(p), y = *reinterpret_cast<const f4u*>(p + 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       v[e] = x[e];
@@ -343,8 +350,8 @@ __device__ __forceinline__ void load_sum(const float* p, float (&v)[VEC]) {
 template <int VEC>
 __device__ __forceinline__ void store_sum(float* p, const float (&v)[VEC]) {
   if constexpr (VEC == 8) {
-    *reinterpret_cast<f4*>(p) = f4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f4*>(p + 4) = f4{v[4], v[5], v[6], v[7]};
+    *reinterpret_cast<f4u*>(p) = f4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f4u*>(p + 4) = f4{v[4], v[5], v[6], v[7]};
   } else {
     p[0] = v[0];
   }
@@ -361,23 +368,37 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const int2* __restr
                                                              float scale, int team, int chunk_tokens, int sum_blocks,
                                                              float* __restrict__ parts, float* __restrict__ dtable) {
   if ((int)blockIdx.x >= sum_blocks) {
-    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * kClearRows, v1 = min<int64_t>(v0 + kClearRows, V);
-    const int64_t c0 = (int64_t)blockIdx.y * team * VEC, c1 = min<int64_t>(c0 + team * VEC, d);
-    for (int64_t v = v0; v < v1; ++v) {
-      if (start[v] != start[v + 1]) continue;
-      if constexpr (VEC == 8) {
-        for (int64_t c = c0 + threadIdx.x * 4; c < c1; c += kThreads * 4) *reinterpret_cast<f4*>(dtable + v * d + c) = f4{};
+    // kClearRows rows are one run of memory that starts 64-byte aligned, whatever
+    // the width: zeros in 16-byte pieces, an element at a time only where a piece
+    // holds entries of two rows
+    __shared__ bool absent[kClearRows + 1];
+    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * kClearRows;
+    const int rows = (int)min<int64_t>(kClearRows, V - v0);
+    if (threadIdx.x <= kClearRows) absent[threadIdx.x] = (int)threadIdx.x < rows && start[v0 + threadIdx.x] == start[v0 + threadIdx.x + 1];
+    __syncthreads();
+    float* const to = dtable + v0 * d;
+    const uint32_t width = (uint32_t)d, entries = (uint32_t)rows * width, pieces = (entries + 3) / 4;
+    const uint32_t first = (uint32_t)((uint64_t)pieces * blockIdx.y / gridDim.y), last = (uint32_t)((uint64_t)pieces * (blockIdx.y + 1) / gridDim.y);
+    for (uint32_t i = first + threadIdx.x; i < last; i += kThreads) {
+      const uint32_t r = 4 * i / width, r3 = (4 * i + 3) / width;   // past the last row: kClearRows or a row that is not there
+      if (r == r3) {
+        if (absent[r]) *reinterpret_cast<f4*>(to + 4 * i) = f4{};
       } else {
-        for (int64_t c = c0 + threadIdx.x; c < c1; c += kThreads) dtable[v * d + c] = 0.0f;
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          const uint32_t re = (4 * i + e) / width;
+          if (re < (uint32_t)rows && absent[re]) to[4 * i + e] = 0.0f;
+        }
       }
     }
     return;
   }
   const int total = start[V];
   const int64_t chunk = (int64_t)blockIdx.x * (kThreads / team) + threadIdx.x / team;
-  const int64_t col = ((int64_t)blockIdx.y * team + threadIdx.x % team) * VEC;
+  const int64_t mine = ((int64_t)blockIdx.y * team + threadIdx.x % team) * VEC, col = min<int64_t>(mine, d - VEC);
+  const int shared = (int)(mine - col);   // columns that the thread before has too
   const int64_t p0 = chunk * chunk_tokens;
-  if (p0 >= total || col >= d) return;
+  if (p0 >= total || mine >= d) return;
   const int count = (int)min<int64_t>(chunk_tokens, total - p0);
   const int id_before = p0 > 0 ? sorted[p0 - 1].y : -1, id_after = p0 + count < total ? sorted[p0 + count].y : -1;
   float acc[VEC];
@@ -418,7 +439,14 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const int2* __restr
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[e] = ADD ? old[ADD ? k : 0][e] + acc[e] * scale : acc[e] * scale;
-        store_sum<VEC>(dtable + (int64_t)ids[k] * d + col, acc);
+        float* const to = dtable + (int64_t)ids[k] * d + col;
+        if (!ADD || shared == 0) {
+          store_sum<VEC>(to, acc);
+        } else {   // its neighbour's columns are added to once
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (e >= shared) to[e] = acc[e];
+        }
       }
       head = false;
 #pragma unroll
@@ -516,7 +544,7 @@ hipError_t launch_bwd(const Id* ids, int64_t T, const _Float16* dout, int64_t V,
     hipLaunchKernelGGL((embed_place_kernel<Id, false>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below, start,
                        sorted);
   }
-  const int vec = d % 8 == 0 ? 8 : 1;
+  const int vec = d >= 8 ? 8 : 1;
   int team = 8;
   while (team < kThreads && team * vec < d) team *= 2;
   const int sum_blocks = (int)((p.chunks + kThreads / team - 1) / (kThreads / team));

@@ -38,7 +38,7 @@ def test_embed_fwd(sp):
     assert call(T=-1) == SHAPE and call(V=-1) == SHAPE and call(d=-8) == SHAPE
     assert call(T=2 ** 31) == TOO_LARGE and call(V=2 ** 31) == TOO_LARGE and call(d=2 ** 31) == TOO_LARGE
     assert call(T=2 ** 30, d=2 ** 10) == TOO_LARGE and call(V=2 ** 30, d=2 ** 10) == TOO_LARGE
-    assert call(T=2 ** 30, d=33) == TOO_LARGE          # 2^35 single entries
+    assert call(T=2 ** 31 - 1, d=128 + 8, V=1) == TOO_LARGE        # over 2^34 chunks of 8 entries
     assert call(ids=None) == NULL and call(table=None) == NULL and call(out=None) == NULL
     assert call(ids=MIS) == ALIGN and call(table=MIS) == ALIGN and call(out=MIS) == ALIGN
     assert call(T=0, ids=None, out=None) == OK and call(d=0, out=None, table=None) == OK
