@@ -141,7 +141,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
+    if stream is None:   # its handle alone: a Stream object would cost more than a launch
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    s = stream
     if s.device.index != torch.cuda.current_device():
         raise ValueError(f"stream is on {s.device} but the current device is cuda:{torch.cuda.current_device()}")
     return ctypes.c_void_p(s.cuda_stream)
