@@ -137,9 +137,11 @@ hipError_t launch_fwd(const void* ids, const void* table, int64_t T, int64_t V, 
 // KiB from L2, less than a launch); beyond, a kernel before it does, once a
 // segment:
 //   count: cnt[seg][v] and below[seg][range]
-constexpr int kRange = 1024, kWaves = kRange / 64, kMinSeg = 2048, kMaxSegs = 16, kSelfCount = 32768;
+constexpr int kRange = 2048, kWaves = 8, kSortThreads = 64 * kWaves, kEach = kRange / kSortThreads;
+constexpr int kMinSeg = 2048, kMaxSegs = 16, kSelfCount = 32768;
 constexpr int kGroups = 4;   // groups of 64 tokens that a wave loads at once
-static_assert(kMinSeg % (64 * kWaves) == 0, "whole waves of tokens");
+constexpr int kIdBits = 11;
+static_assert(kMinSeg % (64 * kWaves) == 0 && 1 << kIdBits == kRange && kEach == 4, "whole waves of tokens, ids in fours");
 
 // What one lane of a wave has written to LDS is read by the others.
 __device__ __forceinline__ void wave_sync() {
@@ -166,10 +168,10 @@ template <typename Id>
 __device__ __forceinline__ int count_tokens(const Id* ids, int t0, int end, uint32_t lo, uint32_t span, int32_t* n) {
   int under = 0;
   constexpr int kLoads = 8;
-  for (int t = t0; t < end; t += kLoads * kRange) {
+  for (int t = t0; t < end; t += kLoads * kSortThreads) {
     uint32_t v[kLoads];
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) v[k] = id_at(ids, t + k * kRange + threadIdx.x, end);
+    for (int k = 0; k < kLoads; ++k) v[k] = id_at(ids, t + k * kSortThreads + threadIdx.x, end);
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       if (v[k] - lo < span) atomicAdd(&n[v[k] - lo], 1);
@@ -180,41 +182,42 @@ __device__ __forceinline__ int count_tokens(const Id* ids, int t0, int end, uint
 }
 
 template <typename Id>
-__global__ __launch_bounds__(kRange) void embed_count_kernel(const Id* __restrict__ ids, int T, int64_t V,
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(const Id* __restrict__ ids, int T, int64_t V,
                                                              int seg_tokens, int32_t* __restrict__ cnt,
                                                              int32_t* __restrict__ below) {
-  __shared__ int32_t n[kRange];
+  __shared__ __align__(16) int32_t n[kRange];
   __shared__ int32_t under;
   const int tid = threadIdx.x;
   const int64_t range = blockIdx.x;
   const int seg = blockIdx.y;
   const uint32_t lo = (uint32_t)(range * kRange), span = (uint32_t)min<int64_t>(kRange, V - lo);
-  n[tid] = 0;
+  reinterpret_cast<int4*>(n)[tid] = int4{};
   if (tid == 0) under = 0;
   __syncthreads();
   const int mine = count_tokens(ids, seg * seg_tokens, min(T, (seg + 1) * seg_tokens), lo, span, n);
   if ((tid & 63) == 0) atomicAdd(&under, mine);
   __syncthreads();
-  cnt[(seg * gridDim.x + range) * kRange + tid] = n[tid];
+  reinterpret_cast<int4*>(cnt)[(seg * gridDim.x + range) * kSortThreads + tid] = reinterpret_cast<const int4*>(n)[tid];
   if (tid == 0) below[seg * gridDim.x + range] = under;
 }
 
 template <typename Id, bool SELF>
-__global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restrict__ ids, int T, int64_t V,
+__global__ __launch_bounds__(kSortThreads) void embed_place_kernel(const Id* __restrict__ ids, int T, int64_t V,
                                                              int seg_tokens, const int32_t* __restrict__ cnt,
                                                              const int32_t* __restrict__ below,
                                                              int32_t* __restrict__ start, int2* __restrict__ sorted) {
-  __shared__ int32_t n[kWaves][kRange];   // counts of each wave's tokens, then where its next one goes
-  __shared__ int32_t others[SELF ? 2 : 1][kRange];
+  // ids in fours, four to a thread
+  __shared__ __align__(16) int32_t n[kWaves][kRange];   // counts of each wave's tokens, then where its next one goes
+  __shared__ __align__(16) int32_t others[SELF ? 2 : 1][SELF ? kRange : 4];
   __shared__ int32_t wave_sum[kWaves], under;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t range = blockIdx.x, ranges = gridDim.x;
   const int seg = blockIdx.y, segs = gridDim.y;
   const uint32_t lo = (uint32_t)(range * kRange), span = (uint32_t)min<int64_t>(kRange, V - lo);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) n[w][tid] = 0;
+  for (int w = 0; w < kWaves; ++w) reinterpret_cast<int4*>(n[w])[tid] = int4{};
   if constexpr (SELF) {
-    others[0][tid] = others[1][tid] = 0;
+    reinterpret_cast<int4*>(others[0])[tid] = reinterpret_cast<int4*>(others[1])[tid] = int4{};
     if (tid == 0) under = 0;
   }
   __syncthreads();
@@ -234,34 +237,46 @@ __global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restric
       if constexpr (SELF) mine += __popcll(__ballot(v[k] < lo));
     }
   }
-  // this thread's id in the segments before and in all
-  int total = 0, before = 0, base = 0;
+  // this thread's ids in the segments before and in all
+  int total[kEach] = {}, before[kEach] = {}, base = 0;
+  const auto add = [](int (&to)[kEach], const int4& v) {
+    to[0] += v.x;
+    to[1] += v.y;
+    to[2] += v.z;
+    to[3] += v.w;
+  };
   if constexpr (SELF) {
     mine += count_tokens(ids, 0, min(T, seg * seg_tokens), lo, span, others[0]);
     mine += count_tokens(ids, (seg + 1) * seg_tokens, T, lo, span, others[1]);
     if (lane == 0) atomicAdd(&under, mine);
     __syncthreads();
-    before = others[0][tid];
-    total = before + others[1][tid];
+    add(before, reinterpret_cast<const int4*>(others[0])[tid]);
+    add(total, reinterpret_cast<const int4*>(others[0])[tid]);
+    add(total, reinterpret_cast<const int4*>(others[1])[tid]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) total += n[w][tid];
+    for (int w = 0; w < kWaves; ++w) add(total, reinterpret_cast<const int4*>(n[w])[tid]);
     base = under;
   } else {
-    int c[kMaxSegs], u[kMaxSegs];   // all loads in flight
+    int4 c[kMaxSegs];   // all loads in flight
+    int u[kMaxSegs];
 #pragma unroll
     for (int s = 0; s < kMaxSegs; ++s) {
-      c[s] = s < segs ? cnt[(s * ranges + range) * kRange + tid] : 0;
-      u[s] = s < segs ? below[s * ranges + range] : 0;
+      const int k = min(s, segs - 1);
+      c[s] = reinterpret_cast<const int4*>(cnt)[(k * ranges + range) * kSortThreads + tid];
+      u[s] = below[k * ranges + range];
     }
 #pragma unroll
     for (int s = 0; s < kMaxSegs; ++s) {
-      total += c[s];
-      if (s < seg) before += c[s];
-      base += u[s];
+      if (s < segs) {
+        add(total, c[s]);
+        base += u[s];
+      }
+      if (s < seg) add(before, c[s]);
     }
   }
   // exclusive scan of the totals over the range's ids
-  int incl = total;
+  const int sum = total[0] + total[1] + total[2] + total[3];
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int up = __shfl_up(incl, o);
@@ -270,17 +285,23 @@ __global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restric
   if (lane == 63) wave_sum[wave] = incl;
   __syncthreads();   // the wave counts are complete as well
   for (int w = 0; w < wave; ++w) base += wave_sum[w];
-  const int first = base + incl - total;
-  if (seg == 0 && tid < (int)span) {
-    start[lo + tid] = first;
-    if ((int64_t)lo + tid == V - 1) start[V] = first + total;
+  int first = base + incl - sum, run[kEach];
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int i = tid * kEach + q;
+    if (seg == 0 && i < (int)span) {
+      start[lo + i] = first;
+      if ((int64_t)lo + i == V - 1) start[V] = first + total[q];
+    }
+    run[q] = first + before[q];
+    first += total[q];
   }
-  int run = first + before;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    const int c = n[w][tid];
-    n[w][tid] = run;
-    run += c;
+    int4* const at = reinterpret_cast<int4*>(n[w]) + tid;
+    const int4 c = *at;
+    *at = make_int4(run[0], run[1], run[2], run[3]);
+    add(run, c);
   }
   __syncthreads();
   for (int t = t0; t < end; t += kGroups * 64) {
@@ -293,7 +314,7 @@ __global__ __launch_bounds__(kRange) void embed_place_kernel(const Id* __restric
       if (same == 0) continue;
       // lanes with this lane's id, by one ballot a bit
 #pragma unroll
-      for (int b = 0; b < 10; ++b) {
+      for (int b = 0; b < kIdBits; ++b) {
         const bool bit = (i >> b) & 1;
         const uint64_t set = __ballot(bit);
         same &= bit ? set : ~set;
@@ -537,11 +558,11 @@ hipError_t launch_bwd(const Id* ids, int64_t T, const _Float16* dout, int64_t V,
   float* parts = reinterpret_cast<float*>(ws + p.parts);
   const dim3 grid((unsigned)p.ranges, (unsigned)p.segs);
   if (T <= kSelfCount) {
-    hipLaunchKernelGGL((embed_place_kernel<Id, true>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, nullptr, nullptr,
+    hipLaunchKernelGGL((embed_place_kernel<Id, true>), grid, dim3(kSortThreads), 0, s, ids, (int)T, V, (int)p.seg_tokens, nullptr, nullptr,
                        start, sorted);
   } else {
-    hipLaunchKernelGGL((embed_count_kernel<Id>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below);
-    hipLaunchKernelGGL((embed_place_kernel<Id, false>), grid, dim3(kRange), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below, start,
+    hipLaunchKernelGGL((embed_count_kernel<Id>), grid, dim3(kSortThreads), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below);
+    hipLaunchKernelGGL((embed_place_kernel<Id, false>), grid, dim3(kSortThreads), 0, s, ids, (int)T, V, (int)p.seg_tokens, cnt, below, start,
                        sorted);
   }
   const int vec = d >= 8 ? 8 : 1;

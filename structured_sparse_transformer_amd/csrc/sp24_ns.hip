@@ -1061,7 +1061,7 @@ using Broad = Tile<128, 256, 64, 64, 3, 2>;
 
 // Items per tile of a reduction over K for a launch of `tiles` tiles: enough
 // to put per_cu on every CU, none shorter than kMinStages.
-constexpr int kMinStages = 8;
+constexpr int kMinStages = 16;
 int splits_for(int64_t tiles, int per_cu, int K) {
   const int64_t want = (int64_t)per_cu * device_cu_count() / tiles, most = K / (kMinStages * kBK);
   const int64_t n = want < most ? want : most;
