@@ -31,6 +31,16 @@
 // A and B are symmetric: only tiles on and above the diagonal are computed,
 // each stored twice.
 //
+// What bounds it.  A step costs m^2 n (A) + m^3 (A^2) + 2 m^2 n (BX) flops: 266
+// GFLOP for five steps of a 1600 x 6400 weight, 192 us at the 1.39 PFLOP/s that
+// a large fp16 library product reaches here.  The products' matrix instructions
+// alone, without loads or LDS reads, run at 1.56 PFLOP/s: under this load the
+// clock is at 1.8 GHz and falls further the busier the units are.  With their
+// operands they reach 0.8 (BX of one weight, 41 us) to 1.0 PFLOP/s (BX of two,
+// 65 us), 0.5 to 0.6 for A and A^2 of 1600 x 1600, which have few tiles.  What
+// the first steps read and write of X's lo part, and the last of P and W, is at
+// memory speed and not hidden where all tiles end together.
+//
 // v_mfma_f32_32x32x16_f16 operands (lane l, g = l / 32):
 //   A: row l % 32, k in [8g, 8g + 8)     B: column l % 32, the same k
 //   D: column l % 32, rows 8*(i/4) + 4g + i%4 for accumulator i
@@ -45,7 +55,6 @@
 namespace sp24 {
 namespace {
 
-typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
@@ -1059,13 +1068,28 @@ template <bool SPLIT> using Small = Tile<64, 128, 32, 64, SPLIT ? 3 : 4, SPLIT ?
 using Tall = Tile<320, 256, 160, 64, 4, 2>;
 using Broad = Tile<128, 256, 64, 64, 3, 2>;
 
-// Items per tile of a reduction over K for a launch of `tiles` tiles: enough
-// to put per_cu on every CU, none shorter than kMinStages.
-constexpr int kMinStages = 16;
-int splits_for(int64_t tiles, int per_cu, int K) {
-  const int64_t want = (int64_t)per_cu * device_cu_count() / tiles, most = K / (kMinStages * kBK);
-  const int64_t n = want < most ? want : most;
-  return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+// Items per tile of A's reduction over `stages` of it, for a launch of `tiles`
+// tiles of `area`: the cheapest by a model of a stage's time on a CU, the items
+// on the fullest CU (side by side they take 0.8 of one after the other; split
+// products have no room for two), and the join, which costs a launch and the
+// traffic of every item's sums.  Measured with the join: one 1600 x 6400 weight
+// 33 us in 5 items a tile, 36 in 2, 38 in 3, 35 in 8; two of them 57 us in 2, 63
+// in 1, 55 in 3.
+int splits_for(int64_t tiles, int64_t area, bool split, int stages) {
+  const double stage = (split ? 0.75e-6 : 0.3e-6) * (area < 128 * 128 ? 0.6 : 1.0), join = 5e-6, rate = 8e12;
+  const int64_t cus = device_cu_count();
+  int best = 1;
+  double best_t = 0.0;
+  for (int n = 1; n <= 16 && (n == 1 || stages / n >= 8); ++n) {
+    const double items = (double)((tiles * n + cus - 1) / cus);
+    const double t = (double)stages / n * stage * items * (items > 1.0 && !split ? 0.8 : 1.0) +
+                     (n > 1 ? join + 2.0 * 4.0 * (double)(tiles * n * area) / rate : 0.0);
+    if (n == 1 || t < best_t) {
+      best = n;
+      best_t = t;
+    }
+  }
+  return best;
 }
 
 template <class T>
@@ -1139,9 +1163,11 @@ int64_t fill(Jobs& large, Jobs& small, const NsJob* in, int count, bool split, u
       continue;
     }
     const int64_t tiles = large.fine ? upper_fine : upper;
-    j.gram_splits = splits_for(tiles, 2, 32 * j.nx);
+    const int64_t area = large.fine ? Small<false>::BM * Small<false>::BN : Square<false>::BM * Square<false>::BN;
+    const int rounded = splits_for(tiles, area, false, j.nx), in_parts = splits_for(tiles, area, true, j.nx);
+    j.gram_splits = rounded > in_parts ? rounded : in_parts;
     at += lay_out(j, large.fine, ws ? ws + at : nullptr);
-    if (split) j.gram_splits = splits_for(tiles, 1, 32 * j.nx);
+    j.gram_splits = split ? in_parts : rounded;
     Jobs& to = !split && is_small<false>(j) ? small : large;
     to.j[to.count++] = j;
   }

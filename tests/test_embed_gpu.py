@@ -195,3 +195,29 @@ def test_same_bits_on_every_run_on_another_stream_and_in_a_graph(sp):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want if k % 2 else -want)
+
+
+def test_offsets_past_32_bits(sp):
+    """A table of 4.3e9 entries: rows beyond 2^32 entries and bytes."""
+    V, d = 70000, 62000
+    ids = dev(np.array([V - 1, 0, 69500, V - 1, 69273, -1]))
+    table = torch.zeros(V, d, dtype=torch.float16, device="cuda")
+    rows = torch.randn(3, d, device="cuda").half()
+    at = torch.tensor([V - 1, 69500, 69273], device="cuda")
+    table[at] = rows
+    out = sp.sp24_embed_fwd(ids, table)
+    zero = torch.zeros(d, dtype=torch.float16, device="cuda")
+    for k, want in enumerate((rows[0], zero, rows[1], rows[0], rows[2], zero)):
+        assert torch.equal(out[k], want)
+    del table
+    dout = torch.randn(6, d, device="cuda").half()
+    grad = torch.full((V, d), float("nan"), device="cuda")
+    sp.sp24_embed_bwd(ids, dout, V, dtable=grad)
+    assert torch.equal(grad[V - 1], dout[0].float() + dout[3].float())
+    assert torch.equal(grad[69500], dout[2].float()) and torch.equal(grad[69273], dout[4].float())
+    assert torch.equal(grad[0], dout[1].float())
+    rest = torch.ones(V, dtype=torch.bool, device="cuda")
+    rest[ids[:5]] = False
+    for lo in range(0, V, 7000):
+        part = grad[lo:lo + 7000]
+        assert (part[rest[lo:lo + 7000]] == 0).all()

@@ -193,8 +193,9 @@ def test_muon_step(sp, shapes, nesterov, precise):
 
 
 def test_steps_of_the_ffn_weights_size(sp):
-    """The widest layer's W2 and a gated layer's W1, each against float64 on the GPU."""
-    for R, C in ((1600, 6400), (3200, 1600)):
+    """The widest layer's W2, a gated layer's W1, a long thin matrix and two ragged ones,
+    each against float64 on the GPU."""
+    for R, C in ((1600, 6400), (3200, 1600), (130, 70001), (2503, 4100), (5000, 2049)):
         gen = torch.Generator(device="cuda").manual_seed(R)
         G = torch.randn(R, C, generator=gen, device="cuda") * 1e-3
         X = G.double() / (G.double().norm() + 1e-7)
@@ -206,3 +207,26 @@ def test_steps_of_the_ffn_weights_size(sp):
         for out in (torch.float16, torch.float32):
             err = ((sp.sp24_orthogonalize(G, dtype=out).double() - X).norm() / X.norm()).item()
             assert err <= tol(out, (R, C))
+
+
+def test_two_large_weights_of_one_call(sp):
+    """Large tiles for the two together, and their steps: against single calls' float64."""
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    shapes = [(1600, 6400), (6400, 1600), (40, 70)]
+    G, M, P = ([torch.randn(*s, generator=gen, device="cuda") * f for s in shapes] for f in (1e-3, 1e-2, 0.02))
+    P0 = [p.double() for p in P]
+    U = [g.double() + 0.95 * (0.95 * m.double() + g.double()) for g, m in zip(G, M)]
+    W = [torch.empty_like(p, dtype=torch.float16) for p in P]
+    sp.sp24_muon_step(G, M, P, W, [0.5] * 3, decays=[0.01] * 3, momentum=0.95)
+    for u, p0, p, w, s in zip(U, P0, P, W, shapes):
+        X = u / (u.norm() + 1e-7)
+        X = X.t().contiguous() if s[0] > s[1] else X
+        for _ in range(5):
+            A = X @ X.t().contiguous()
+            X = COEFFS[0] * X + (COEFFS[1] * A + COEFFS[2] * (A @ A)) @ X
+        X = X.t() if s[0] > s[1] else X
+        step = 0.5 * X.norm()
+        err = (p.double() - (0.99 * p0 - 0.5 * X)).norm()
+        # momentum and nesterov in fp32: the update's direction to 2^-22
+        assert err <= tol(torch.float16, s) * step + 3 * 2.0 ** -24 * (p0.norm() + step)
+        assert torch.equal(w, p.half())
