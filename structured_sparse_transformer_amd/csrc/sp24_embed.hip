@@ -9,7 +9,15 @@
 //
 // The gradient sorts the tokens by id (stably, so that every row's sum runs in
 // token order and results do not depend on timing), then sums runs of equal
-// ids.  No atomics on floating point, no dense [T, V] anything.
+// ids.  No atomics on floating point, no dense [T, V] anything.  Sums are held
+// in fp32.
+//
+// Both move bytes and nothing else.  At 16384 tokens, width 1600 and 50257 rows
+// the forward from an fp32 table takes 18 us (5.0 TB/s; a large copy reaches
+// 5.1), the dense gradient 9 us to sort, 64 to sum and clear (5.8 TB/s, of which
+// 86% are writes) and 6 to join the runs that chunks cut.  131072 tokens of
+// width 1024 added to a gradient: 27, 93 (4.2 TB/s: rows of 2 and 4 KiB in the
+// ids' order, a quarter of them read and written back) and 13 us.
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
@@ -49,7 +57,8 @@ __device__ __forceinline__ void load_row8<float>(const float* p, float (&v)[8]) 
   }
 }
 
-// A row is d / VEC chunks, rounded up; a workgroup takes kThreads * kItems
+// One gather per item from a row that its id names; kItems of them in flight a
+// thread.  A row is d / VEC chunks, rounded up; a workgroup takes kThreads * kItems
 // consecutive chunks of all rows'.
 template <typename Table, typename Id, int VEC>
 __global__ __launch_bounds__(kThreads) void embed_fwd_kernel(const Id* __restrict__ ids, const Table* __restrict__ table,

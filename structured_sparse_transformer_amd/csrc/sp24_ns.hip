@@ -21,9 +21,9 @@
 //             the epilogue, from both parts: there the small singular values
 //             grow 3.4 times a step, and with them the rounding error of X,
 //             which costs up to 6e-3 of the result's norm on a low-rank update
-//             if neither step does so, and 1.5e-3 after two that do.  Results
-//             are within about 2e-3 of exact arithmetic (bf16 operands: 1e-2
-//             to 5e-2).
+//             if neither step does so, and 1.5 to 2.4e-3 after two that do.
+//             Results are within about 2.5e-3 of exact arithmetic (bf16
+//             operands: 1e-2 to 5e-2).
 //   split     hi hi + hi lo + lo hi, for results to fp32 accuracy.
 // All other steps have a I in B (Q = a I + B, X <- Q X), so that the last
 // product of a step reads X once and writes what the next one needs.
@@ -37,9 +37,10 @@
 // alone, without loads or LDS reads, run at 1.56 PFLOP/s: under this load the
 // clock is at 1.8 GHz and falls further the busier the units are.  With their
 // operands they reach 0.8 (BX of one weight, 41 us) to 1.0 PFLOP/s (BX of two,
-// 65 us), 0.5 to 0.6 for A and A^2 of 1600 x 1600, which have few tiles.  What
-// the first steps read and write of X's lo part, and the last of P and W, is at
-// memory speed and not hidden where all tiles end together.
+// 65 us), 0.5 for A (34 us with its join) and 0.3 for A^2 (15 us) of
+// 1600 x 1600, which have few tiles.  What the first steps read and write
+// of X's lo part, and the last of P and W, is at memory speed and not hidden
+// where all tiles end together.
 //
 // v_mfma_f32_32x32x16_f16 operands (lane l, g = l / 32):
 //   A: row l % 32, k in [8g, 8g + 8)     B: column l % 32, the same k
@@ -171,7 +172,9 @@ __device__ __forceinline__ double block_sum(double v) {
 
 // Momentum, and the squares of the update summed in 64 bits (a sum of fp32
 // squares would lose updates below 1e-22 or above 1e19).  Eight entries a
-// thread at a time; a workgroup takes kNormChunk of them.
+// thread at a time; a workgroup takes kNormChunk of them.  Memory-bound: 49 us
+// (4.2 TB/s) for the momentum of 6400 x 1600 and 1600 x 6400, 9 us for the norm
+// of one 1600 x 6400 in fp16.
 __global__ __launch_bounds__(kThreads) void ns_norm_kernel(Jobs jobs, float mu, bool nesterov) {
   const Job& j = job_of(jobs, blockIdx.x);
   const int block = blockIdx.x - j.first;
@@ -232,7 +235,8 @@ __device__ __forceinline__ void put8(_Float16* p, int64_t plane, bool both, cons
 }
 
 // X_0 in both parts, 32 x 64 of it a workgroup (two blocks side by side);
-// zeros past m and n.
+// zeros past m and n.  Memory-bound: 54 us (3.8 TB/s) for those two weights, 20
+// for the one; a pass of its own because it needs the norm of all of U.
 __global__ __launch_bounds__(kThreads) void ns_start_kernel(Jobs jobs, float mu, bool nesterov, float eps) {
   __shared__ float tile[64][33];
   const Job& j = job_of(jobs, blockIdx.x);
@@ -738,7 +742,10 @@ __global__ __launch_bounds__(64 * T::WAVES, T::OCC) void ns_product_kernel(Jobs 
   }(std::make_integer_sequence<int, T::TM * T::TN / 2>{});
 }
 
-// Adds up the shares of split reductions, in their order, 32 x 64 a wave.
+// Adds up the shares of split reductions, in their order, 32 x 64 a wave.  8 us
+// for 5 shares of a 1600 x 1600 A (30 MB).  With the last item of a tile to
+// arrive adding them up in the product's launch, the two took 52 us together,
+// here 34.
 template <bool SPLIT, class T>
 __global__ __launch_bounds__(64 * T::WAVES) void ns_join_kernel(Jobs jobs, Step st) {
   __shared__ __align__(16) float smem[T::WAVES * 32 * kTurn];
@@ -774,7 +781,8 @@ __global__ __launch_bounds__(64 * T::WAVES) void ns_join_kernel(Jobs jobs, Step 
 // All of a small weight's steps in one workgroup, with X, A and B in LDS, in the
 // blocks and swizzle that a stage of the large products has there.  A chain of
 // launches takes 4 us a product whatever its size; 64 x 64 and five steps took
-// 76 us of them.  Every product's tiles are made with the operands such that a
+// 76 us of them, and 18 here.  What is left is latency: each step's three
+// products wait for LDS and for each other.  Every product's tiles are made with the operands such that a
 // lane ends up with four neighbours of a row of the result: of A and B, which
 // are symmetric, both halves are computed; of X, a wave makes whole columns of
 // blocks, which nothing else reads, and puts them back in place.
