@@ -460,8 +460,8 @@ int sp24_embed_fwd(const void* ids, int id_type, int64_t T, const void* table, i
  *   dtable     out     fp32 [V, d] (in/out with accumulate)
  *   workspace  scratch device memory of sp24_embed_bwd_workspace bytes
  * Errors: NULL, SHAPE, ALIGN, LAUNCH; UNSUPPORTED for another id type;
- * WORKSPACE when workspace_bytes is too few; TOO_LARGE when T reaches 2^28, d
- * 2^24, V 2^31, or a matrix 2^40 entries.
+ * WORKSPACE when workspace_bytes is too few; TOO_LARGE when T reaches 2^28, V
+ * 2^27, d 2^24 - 256, or a matrix 2^40 entries.
  */
 int sp24_embed_bwd(const void* ids, int id_type, int64_t T, const void* dout, int64_t V, int64_t d, float scale,
                    int accumulate, float* dtable, void* workspace, int64_t workspace_bytes, void* stream);

@@ -93,13 +93,16 @@ int check_geglu(int64_t T, int64_t h, int64_t group) {
   return SP24_OK;
 }
 
-constexpr int64_t kMaxEmbedTokens = (int64_t)1 << 28, kMaxEmbedWidth = (int64_t)1 << 24;
+// The gradient's launches: 256 work-items for 16 rows to clear beside those of
+// the chunks, 65535 workgroups of 256 columns.
+constexpr int64_t kMaxEmbedTokens = (int64_t)1 << 28, kMaxEmbedRows = (int64_t)1 << 27,
+                  kMaxEmbedWidth = ((int64_t)1 << 24) - 256;
 
 int check_embed_bwd(int64_t T, int64_t V, int64_t d) {
   int st = check_dims(T, d, 1);
   if (st != SP24_OK) return st;
   if ((st = check_dims(V, d, 1)) != SP24_OK) return st;
-  return T >= kMaxEmbedTokens || d >= kMaxEmbedWidth ? SP24_ERR_TOO_LARGE : SP24_OK;
+  return T >= kMaxEmbedTokens || V >= kMaxEmbedRows || d >= kMaxEmbedWidth ? SP24_ERR_TOO_LARGE : SP24_OK;
 }
 
 int check_ns_shape(int64_t R, int64_t C) {

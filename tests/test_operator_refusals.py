@@ -64,6 +64,16 @@ def test_embed_bwd(sp):
     assert size(2 ** 28, 10, 8) == -1 and size(-1, 10, 8) == -1
 
 
+def test_embed_bwd_stays_within_a_launch(sp):
+    # a launch has 2^32 work-items along x (clearing takes 256 for 16 rows, placing
+    # 512 for 2048 ids) and 65535 workgroups along y (joining takes 256 columns each)
+    size = sp.lib().sp24_embed_bwd_workspace
+    assert size(10, 2 ** 27 - 1, 1) > 0 and size(10, 2 ** 27, 1) == -1 and size(10, 2 ** 28, 1) == -1
+    assert (2 ** 22 + 2 ** 27 // 16) * 256 < 2 ** 32 and (2 ** 28 // 64) * 512 < 2 ** 32
+    assert size(10, 10, 2 ** 24 - 257) > 0 and size(10, 10, 2 ** 24 - 256) == -1
+    assert -(-(2 ** 24 - 257) // 256) <= 65535
+
+
 def ortho_jobs(sp, *jobs):
     return (sp.OrthoJob * len(jobs))(*[sp.OrthoJob(*j) for j in jobs])
 
