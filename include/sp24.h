@@ -428,6 +428,9 @@ enum {
   SP24_I64 = 3
 };
 
+/* May be added to sp24_orthogonalize's out_type: products of fp16 operands. */
+enum { SP24_FP16_OPERANDS = 16 };
+
 /*
  * Token embedding: out[t] = scale * table[ids[t]], rounded to nearest even in
  * fp16.  It makes the FFN path's input from token ids.  An id outside [0, V)
@@ -478,11 +481,13 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  * the usual (3.4445, -4.7750, 2.0315), five times, brings all but the
  * smallest to about 1.  A zero update gives zeros (for eps > 0).
  *
- * out_type SP24_F16: the products' operands are rounded to fp16 (at a scale
- * that keeps their full precision); fp32 sums.  With the usual coefficients
- * the result is within about 2e-3 of exact arithmetic, normwise.
- * out_type SP24_F32: operands in two fp16 parts, three products each, for
- * results to about fp32's own accuracy.
+ * The products' operands are held in two fp16 parts, three products each with
+ * fp32 sums, for results to about fp32's own accuracy; of out_type SP24_F16
+ * they are rounded once at the end.  With SP24_FP16_OPERANDS added to out_type
+ * the operands are rounded to fp16 (at a scale that keeps their full
+ * precision), for a third of the matrix work: with the usual coefficients a
+ * result of either type is then within about 2e-3 of exact arithmetic,
+ * normwise.
  *
  *   jobs       in    host array: G [R, C] of g_type, out [R, C] of out_type
  *                    (may be G's own memory when the types agree)
@@ -529,7 +534,8 @@ int64_t sp24_orthogonalize_workspace(const sp24_ortho_job* jobs, int count);
  *     lr, decay       the update's factor (with any factor for the weight's
  *                     shape) and the part of P that is taken off (lr times
  *                     the weight decay)
- *   precise != 0: products of two-part operands, as for SP24_F32 results
+ *   precise != 0: operands in two parts; 0: fp16 ones, as SP24_FP16_OPERANDS
+ *                 says
  *   coef, steps, eps, workspace, errors: as sp24_orthogonalize
  */
 typedef struct sp24_muon_job {

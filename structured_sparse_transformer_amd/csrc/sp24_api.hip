@@ -355,12 +355,14 @@ int sp24_orthogonalize(const sp24_ortho_job* jobs, int count, int g_type, int ou
                        float eps, void* workspace, int64_t workspace_bytes, void* stream) {
   if (jobs == nullptr) return SP24_ERR_NULL;
   if (count < 1 || count > SP24_MAX_BATCH) return SP24_ERR_SHAPE;
+  const bool rounded = (out_type & SP24_FP16_OPERANDS) != 0;
+  out_type &= ~SP24_FP16_OPERANDS;
   if ((g_type != SP24_F16 && g_type != SP24_F32) || (out_type != SP24_F16 && out_type != SP24_F32))
     return SP24_ERR_UNSUPPORTED;
   sp24::NsParams prm{};
   int st = ns_params(coef, steps, eps, prm);
   if (st != SP24_OK) return st;
-  prm.split = out_type == SP24_F32;
+  prm.split = !rounded;
   sp24::NsJob d[SP24_MAX_BATCH] = {};
   for (int k = 0; k < count; ++k) {
     const sp24_ortho_job& j = jobs[k];

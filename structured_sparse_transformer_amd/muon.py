@@ -26,10 +26,11 @@ from . import sp24
 
 class Muon:
     """``weights``: the fp16 weights of the layers, updated in place; the
-    masters start as their values unless given."""
+    masters start as their values unless given.  ``precise=False`` orthogonalises
+    with products of fp16 operands, a third of the matrix work."""
 
     def __init__(self, weights, masters=None, lr: float = 3e-4, momentum: float = 0.95, weight_decay: float = 0.0,
-                 nesterov: bool = True, steps: int = 5, coeffs=None, precise: bool = False):
+                 nesterov: bool = True, steps: int = 5, coeffs=None, precise: bool = True):
         self.weights = list(weights)
         self.masters = [w.float() for w in self.weights] if masters is None else list(masters)
         self.momenta = [torch.zeros_like(p) for p in self.masters]

@@ -40,6 +40,7 @@ MAX_GROUP = 8
 GROUP_WORKSPACE_BYTES = 64
 MAX_NS_STEPS = 32
 F16, F32, I32, I64 = 0, 1, 2, 3
+FP16_OPERANDS = 16
 # the usual quintic of the Newton-Schulz iteration: five steps bring singular
 # values to about [0.7, 1.2]
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -525,11 +526,12 @@ def _coeffs(coeffs, steps):
 
 
 def sp24_orthogonalize_batch(Gs, steps=5, coeffs=None, eps=1e-7, dtype=torch.float16, outs=None, workspace=None,
-                             stream=None):
+                             stream=None, precise=True):
     """The orthogonalised updates of up to 8 weights (all float16 or all
     float32, [R, C] each) by `steps` Newton-Schulz steps, in one sequence of
-    launches.  ``dtype`` float16: products of fp16 operands; float32: to
-    float32's accuracy, at about three times the work."""
+    launches.  The results are of ``dtype``, float16 or float32, computed to
+    float32's accuracy and rounded once; ``precise=False`` takes products of
+    fp16 operands, a third of the matrix work."""
     if not 1 <= len(Gs) <= MAX_BATCH:
         raise ValueError(f"between 1 and {MAX_BATCH} updates per batch")
     types = {torch.float16: F16, torch.float32: F32}
@@ -549,22 +551,26 @@ def sp24_orthogonalize_batch(Gs, steps=5, coeffs=None, eps=1e-7, dtype=torch.flo
     with _using(stream):
         workspace = _workspace(workspace, lib().sp24_orthogonalize_workspace(arr, len(Gs)), Gs[0].device)
     _check("sp24_orthogonalize", lib().sp24_orthogonalize(
-        arr, len(Gs), types[Gs[0].dtype], types[dtype], ctypes.cast(coef, ctypes.c_void_p), steps, float(eps),
+        arr, len(Gs), types[Gs[0].dtype], types[dtype] | (0 if precise else FP16_OPERANDS),
+        ctypes.cast(coef, ctypes.c_void_p), steps, float(eps),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
     return res
 
 
-def sp24_orthogonalize(G, steps=5, coeffs=None, eps=1e-7, dtype=torch.float16, out=None, workspace=None, stream=None):
+def sp24_orthogonalize(G, steps=5, coeffs=None, eps=1e-7, dtype=torch.float16, out=None, workspace=None, stream=None,
+                       precise=True):
     """sp24_orthogonalize_batch of one update."""
-    return sp24_orthogonalize_batch([G], steps, coeffs, eps, dtype, None if out is None else [out], workspace, stream)[0]
+    return sp24_orthogonalize_batch([G], steps, coeffs, eps, dtype, None if out is None else [out], workspace, stream,
+                                    precise)[0]
 
 
 def sp24_muon_step(Gs, Ms, Ps, Ws, lrs, decays=None, momentum=0.95, nesterov=True, steps=5, coeffs=None, eps=1e-7,
-                   precise=False, workspace=None, stream=None):
+                   precise=True, workspace=None, stream=None):
     """One optimiser step of up to 8 weights, in place: momentum Ms[k] and
     weights Ps[k] (float32 [R, C]) from the gradient Gs[k] (float32), and
     Ws[k] (float16, or None) = Ps[k].  lrs[k] multiplies the orthogonalised
-    update, 1 - decays[k] the weight."""
+    update, 1 - decays[k] the weight.  ``precise`` as sp24_orthogonalize_batch
+    takes it."""
     n = len(Gs)
     if not 1 <= n <= MAX_BATCH:
         raise ValueError(f"between 1 and {MAX_BATCH} weights per step")
