@@ -483,11 +483,21 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  *
  * The products' operands are held in two fp16 parts, three products each with
  * fp32 sums, for results to about fp32's own accuracy; of out_type SP24_F16
- * they are rounded once at the end.  With SP24_FP16_OPERANDS added to out_type
- * the operands are rounded to fp16 (at a scale that keeps their full
- * precision), for a third of the matrix work: with the usual coefficients a
- * result of either type is then within about 2e-3 of exact arithmetic,
- * normwise.
+ * they are rounded once at the end.  With the usual coefficients an update of
+ * full rank comes within about 1e-5 of exact arithmetic in five steps,
+ * normwise.  In directions that an update lacks, a step multiplies rounding
+ * errors by a, here as in fp32 arithmetic: any update, of rank one too, comes
+ * within 3e-6 a^(steps - 1) (4e-4 in five steps, 2e-2 in eight).
+ *
+ * With SP24_FP16_OPERANDS added to out_type the products' operands are rounded
+ * to fp16 (at a scale that keeps their full precision; X itself keeps two
+ * parts), for a third of the matrix work.  A result of either type is then off
+ * by up to 6e-4 more a step, normwise, where the update's short side is 128 or
+ * more (3e-3 in five steps), and by up to 3e-3 a step where few roundings
+ * average out: with a shorter side, or entries all alike or mostly zero.
+ *
+ * X is held to 2^-36 in absolute terms: an update whose norm is far below eps
+ * loses its last bits, and below about 1e-11 eps all of them.
  *
  *   jobs       in    host array: G [R, C] of g_type, out [R, C] of out_type
  *                    (may be G's own memory when the types agree)

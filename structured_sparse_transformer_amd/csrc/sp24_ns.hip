@@ -14,33 +14,51 @@
 // Number formats.  X, A and B are held as fp16 in units of 2^-12.  The
 // entries of X are about (m n)^-1/2 at the start (3e-4 for a 1600 x 6400
 // weight), where fp16 itself has few or no bits left; in these units values
-// up to 16 fit and the typical ones keep all 11 bits.  Beside the rounded
-// part hi, X keeps the rest lo = fp16(x - hi), 22 bits together.  Products are
-// accumulated in fp32 in either mode:
-//   rounded   products of the hi parts.  The first kLoSteps steps take a X in
-//             the epilogue, from both parts: there the small singular values
-//             grow 3.4 times a step, and with them the rounding error of X,
-//             which costs up to 6e-3 of the result's norm on a low-rank update
-//             if neither step does so, and 1.5 to 2.4e-3 after two that do.
-//             Results are within about 2.5e-3 of exact arithmetic (bf16
-//             operands: 1e-2 to 5e-2).
-//   split     hi hi + hi lo + lo hi, for results to fp32 accuracy.
-// All other steps have a I in B (Q = a I + B, X <- Q X), so that the last
-// product of a step reads X once and writes what the next one needs.
+// below 16 fit and the typical ones keep all 11 bits.  Beside the rounded
+// part hi, X keeps the rest lo = fp16(x - hi), 22 bits together; values below
+// 2^-36 are lost.  Products are accumulated in fp32 in either mode:
+//   split     hi hi + hi lo + lo hi, for results to fp32 accuracy.  B has a I
+//             in it (Q = a I + B, X <- Q X), so that the last product of a step
+//             reads X once.
+//   rounded   products of the hi parts, when the caller asks for them: a third
+//             of the matrix work.  Every step takes a X in the epilogue, from
+//             both parts.  A step multiplies what X has in directions that the
+//             update lacks by a (3.4): X's rounding to 11 bits would be 1.4e-2
+//             of a rank-one result after five steps and 0.36 after eight, that
+//             to 22 bits is 1e-4 and 3e-3, in either mode and as in fp32.  The
+//             roundings of A and B and of X inside the products do not grow
+//             so: what they change of B X has the update's rows or its columns,
+//             and no new direction of both.  Where singular values are nearly
+//             equal B is nearly a multiple of I, and its diagonal's roundings
+//             are all the same one: that part of them is taken along, row by
+//             row, with a X (2.9e-3 without it in five steps of equal values of
+//             a 300 x 900 weight).  The rest costs up to 6e-4 of the norm a
+//             step where the short side is 128 or more (largest of an emulation
+//             over spectra from one value to all equal: 5.3e-4), and up to
+//             3e-3 where few roundings average out: small weights, and entries
+//             that are all alike or mostly zero.
 //
 // A and B are symmetric: only tiles on and above the diagonal are computed,
 // each stored twice.
 //
-// What bounds it.  A step costs m^2 n (A) + m^3 (A^2) + 2 m^2 n (BX) flops: 266
-// GFLOP for five steps of a 1600 x 6400 weight, 192 us at the 1.39 PFLOP/s that
-// a large fp16 library product reaches here.  The products' matrix instructions
-// alone, without loads or LDS reads, run at 1.56 PFLOP/s: under this load the
-// clock is at 1.8 GHz and falls further the busier the units are.  With their
-// operands they reach 0.8 (BX of one weight, 41 us) to 1.0 PFLOP/s (BX of two,
-// 65 us), 0.5 for A (34 us with its join) and 0.3 for A^2 (15 us) of
-// 1600 x 1600, which have few tiles.  What the first steps read and write
-// of X's lo part, and the last of P and W, is at memory speed and not hidden
-// where all tiles end together.
+// What bounds it.  A step costs m^2 n (A) + m^3 (A^2) + 2 m^2 n (BX) flops, in
+// two parts three times that: 266 GFLOP for five steps of a 1600 x 6400 weight,
+// 192 us (in two parts 574) at the 1.39 PFLOP/s that a large fp16 library
+// product reaches here.  Medians of the kernels at that size over several cards,
+// in us, with the rate in PFLOP/s and the share of cycles in which the matrix
+// units are busy:
+//                   two parts                        fp16 operands
+//   B X             113 - 116      0.85 - 0.87  0.41   46 - 47       0.70 - 0.71  0.32
+//   B X of two      189 - 198      0.99 - 1.04  0.53   82 - 86       0.77 - 0.80  0.35
+//   A and its join  58 + 9         0.73         0.43   25 + 8        0.50         0.29
+//   A^2             25 - 26        0.48         0.19   15            0.27         0.09
+// The matrix instructions alone, without loads or LDS reads, run at 1.56
+// PFLOP/s, the clock down to 1.8 GHz.  What keeps the products from that: the
+// latency of a stage's LDS reads and its barrier, with 24 MFMAs a wave between
+// two of them (12 in A^2; of fp16 operands 8 and 4) and in two parts one
+// workgroup a CU; few tiles (650 of one weight's B X, 181 of A^2, on 256 CUs);
+// and at the ends, where all tiles come together, the traffic of X's parts and
+// in the last step of P and W.
 //
 // v_mfma_f32_32x32x16_f16 operands (lane l, g = l / 32):
 //   A: row l % 32, k in [8g, 8g + 8)     B: column l % 32, the same k
@@ -65,7 +83,6 @@ typedef __attribute__((address_space(3))) s4 lds_s4;
 
 constexpr int kThreads = 256;
 constexpr float kScale = 4096.0f, kInvScale = 1.0f / 4096.0f;   // the units of X, A and B
-constexpr int kLoSteps = 2;
 constexpr int kNormChunk = 16 * kThreads;   // entries a workgroup squares at a time
 constexpr int kMaxParts = 1024;             // partial sums of squares per weight
 constexpr int kBK = 32;            // reduction per stage
@@ -172,9 +189,9 @@ __device__ __forceinline__ double block_sum(double v) {
 
 // Momentum, and the squares of the update summed in 64 bits (a sum of fp32
 // squares would lose updates below 1e-22 or above 1e19).  Eight entries a
-// thread at a time; a workgroup takes kNormChunk of them.  Memory-bound: 49 us
-// (4.2 TB/s) for the momentum of 6400 x 1600 and 1600 x 6400, 9 us for the norm
-// of one 1600 x 6400 in fp16.
+// thread at a time; a workgroup takes kNormChunk of them.  Memory-bound: 46 to 49
+// us (4.2 to 4.4 TB/s) for the momentum of 6400 x 1600 and 1600 x 6400, 9 us for
+// the norm of one.
 __global__ __launch_bounds__(kThreads) void ns_norm_kernel(Jobs jobs, float mu, bool nesterov) {
   const Job& j = job_of(jobs, blockIdx.x);
   const int block = blockIdx.x - j.first;
@@ -235,8 +252,9 @@ __device__ __forceinline__ void put8(_Float16* p, int64_t plane, bool both, cons
 }
 
 // X_0 in both parts, 32 x 64 of it a workgroup (two blocks side by side);
-// zeros past m and n.  Memory-bound: 54 us (3.8 TB/s) for those two weights, 20
-// for the one; a pass of its own because it needs the norm of all of U.
+// zeros past m and n.  Memory-bound: 48 to 51 us (3.9 to 4.3 TB/s) for those two
+// weights, 19 for the one; a pass of its own because it needs the norm of all of
+// U.
 __global__ __launch_bounds__(kThreads) void ns_start_kernel(Jobs jobs, float mu, bool nesterov, float eps) {
   __shared__ float tile[64][33];
   const Job& j = job_of(jobs, blockIdx.x);
@@ -358,17 +376,17 @@ __device__ __forceinline__ void upper_tile(int m, int k, int& tm, int& tn) {
 struct Step {
   int cur;          // which of x[] holds X
   float a, b, c;
-  bool in_q;        // a I is in B
-  bool write_lo;    // the next step needs X's lo part
 };
 
 // The end of a product for 32 rows from r0 and 64 columns from c0 of its result,
-// in a wave's accumulators v0 and v1 (32 columns each): A; B = b A + c v, with
-// a I or without; X <- a X + v (ADD) or v; or the outcome of the last step.  They are turned through the
-// wave's block of LDS, so that a lane holds 8 columns of a row and what it reads
-// and writes is whole 16-byte pieces of contiguous runs.  What goes out
-// transposed (the mirrored tile, a tall weight) is put back and read by columns.
-template <int KIND, bool SPLIT, bool LAST, bool ADD>
+// in a wave's accumulators v0 and v1 (32 columns each): A; B = b A + c v, plus
+// a I if split; X <- v if split, else (a + d) X + v with d what rounding took off
+// B's diagonal; or the outcome of the last step.
+// They are turned through the wave's block of LDS, so that a lane holds 8
+// columns of a row and what it reads and writes is whole 16-byte pieces of
+// contiguous runs.  What goes out transposed (the mirrored tile, a tall weight)
+// is put back and read by columns.
+template <int KIND, bool SPLIT, bool LAST>
 __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror, int r0, int c0, const f16v& v0,
                                        const f16v& v1, float* turn, int lane) {
   const int g = lane >> 5, l32 = lane & 31, er = lane >> 3, ec = (lane & 7) * 8;
@@ -379,15 +397,18 @@ __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror
   const int64_t plane = (int64_t)j.na * nb * 1024;
   const bool in = r0 < 32 * j.na && c0 + ec < 32 * nb;
   const int64_t at0 = at_block(r0 + er, c0 + ec, nb);   // rows 8 apart are 256 elements apart
-  constexpr bool kLoads = KIND == kPoly || ADD;
+  constexpr bool kAddX = KIND == kApply && !SPLIT, kLoads = KIND == kPoly || kAddX;
   h8 ohi[4], olo[4];
+  float rest = 0.0f;   // of B's diagonal, for row l32 of the 32
+  if constexpr (kAddX)
+    if (r0 < 32 * j.na) rest = (float)j.B[(int64_t)j.na * j.na * 1024 + at_block(r0 + l32, r0 + l32, j.na)] * kInvScale;
   if constexpr (kLoads) {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       ohi[p] = olo[p] = h8{};
       if (in) {
         ohi[p] = *reinterpret_cast<const h8*>(old + at0 + p * 256);
-        if constexpr (SPLIT || ADD) olo[p] = *reinterpret_cast<const h8*>(old + at0 + p * 256 + plane);
+        if constexpr (SPLIT || kAddX) olo[p] = *reinterpret_cast<const h8*>(old + at0 + p * 256 + plane);
       }
     }
   }
@@ -427,20 +448,21 @@ __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror
   for (int p = 0; p < 4; ++p) {
     float* const mine = turn + (p * 8 + er) * kTurn + ec;
     const f4 x = *reinterpret_cast<const f4*>(mine), y = *reinterpret_cast<const f4*>(mine + 4);
+    const float a = kAddX ? st.a + __shfl(rest, p * 8 + er) : st.a;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = (e < 4 ? x[e & 3] : y[e & 3]) * kInvScale;
       if constexpr (kLoads) {
         const float was = (float)ohi[p][e] + (float)olo[p][e];
-        v[e] = KIND == kPoly ? st.b * was + st.c * v[e] : st.a * was + v[e];
-        if constexpr (KIND == kPoly)
-          if (st.in_q && r0 + p * 8 + er == c0 + ec + e) v[e] += st.a * kScale;
+        v[e] = KIND == kPoly ? st.b * was + st.c * v[e] : a * was + v[e];
+        if constexpr (KIND == kPoly && SPLIT)
+          if (r0 + p * 8 + er == c0 + ec + e) v[e] += a * kScale;
       }
       if constexpr (LAST) v[e] *= kInvScale;
     }
     if constexpr (!LAST)
-      if (in) put8(D + at0 + p * 256, plane, SPLIT || (KIND == kApply && st.write_lo), v);
+      if (in) put8(D + at0 + p * 256, plane, SPLIT || KIND == kApply || (KIND == kPoly && !mirror), v);
     if (LAST || by_col) {
       *reinterpret_cast<f4*>(mine) = f4{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f4*>(mine + 4) = f4{v[4], v[5], v[6], v[7]};
@@ -491,7 +513,7 @@ __device__ __forceinline__ void finish(const Job& j, const Step& st, bool mirror
   wave_sync();   // the block has been read
 }
 
-template <int KIND, bool SPLIT, bool LAST, bool ADD, class T>
+template <int KIND, bool SPLIT, bool LAST, class T>
 __global__ __launch_bounds__(64 * T::WAVES, T::OCC) void ns_product_kernel(Jobs jobs, Step st) {
   constexpr int PARTS = SPLIT ? 2 : 1;
   constexpr int LEFT = T::BM * kBK * 2, RIGHT = T::BN * kBK * 2;   // bytes of one operand's part
@@ -734,7 +756,7 @@ __global__ __launch_bounds__(64 * T::WAVES, T::OCC) void ns_product_kernel(Jobs 
     (
         [&]() __attribute__((always_inline)) {
           constexpr int s = I / (T::TN / 2), t = I % (T::TN / 2) * 2;
-          finish<KIND, SPLIT, LAST, ADD>(j, st, mirror, m0 + wm * T::WM + s * 32, n0 + wn * T::WN + t * 32, acc[s][t],
+          finish<KIND, SPLIT, LAST>(j, st, mirror, m0 + wm * T::WM + s * 32, n0 + wn * T::WN + t * 32, acc[s][t],
                                          acc[s][t + 1], turn, lane);
           __builtin_amdgcn_sched_barrier(0);   // one block's registers at a time
         }(),
@@ -742,10 +764,10 @@ __global__ __launch_bounds__(64 * T::WAVES, T::OCC) void ns_product_kernel(Jobs 
   }(std::make_integer_sequence<int, T::TM * T::TN / 2>{});
 }
 
-// Adds up the shares of split reductions, in their order, 32 x 64 a wave.  8 us
-// for 5 shares of a 1600 x 1600 A (30 MB).  With the last item of a tile to
-// arrive adding them up in the product's launch, the two took 52 us together,
-// here 34.
+// Adds up the shares of split reductions, in their order, 32 x 64 a wave.  8 to
+// 9 us for those of a 1600 x 1600 A.  With the last item of a tile to arrive
+// adding them up in the product's launch, the two took 52 us together, here 33
+// (fp16 operands).
 template <bool SPLIT, class T>
 __global__ __launch_bounds__(64 * T::WAVES) void ns_join_kernel(Jobs jobs, Step st) {
   __shared__ __align__(16) float smem[T::WAVES * 32 * kTurn];
@@ -774,16 +796,16 @@ __global__ __launch_bounds__(64 * T::WAVES) void ns_join_kernel(Jobs jobs, Step 
       for (int e = 0; e < 4; ++e) acc[q >> 2][4 * (q & 3) + e] += v[e];
     }
   }
-  finish<kGram, SPLIT, false, false>(j, st, tn != tm / (T::BN / T::BM), tm * T::BM + wave % T::WAVES_M * T::WM + s * 32,
+  finish<kGram, SPLIT, false>(j, st, tn != tm / (T::BN / T::BM), tm * T::BM + wave % T::WAVES_M * T::WM + s * 32,
                              tn * T::BN + wave / T::WAVES_M * T::WN + t * 32, acc[0], acc[1], smem + wave * (32 * kTurn), lane);
 }
 
 // All of a small weight's steps in one workgroup, with X, A and B in LDS, in the
 // blocks and swizzle that a stage of the large products has there.  A chain of
 // launches takes 4 us a product whatever its size; 64 x 64 and five steps took
-// 76 us of them, and 18 here.  What is left is latency: each step's three
-// products wait for LDS and for each other.  Every product's tiles are made with the operands such that a
-// lane ends up with four neighbours of a row of the result: of A and B, which
+// 76 us of them, and 23 here (fp16 operands: 21).  What is left is latency: each
+// step's three products wait for LDS and for each other.  Every product's tiles
+// are made with the operands such that a lane ends up with four neighbours of a row of the result: of A and B, which
 // are symmetric, both halves are computed; of X, a wave makes whole columns of
 // blocks, which nothing else reads, and puts them back in place.
 constexpr int kSmallThreads = 512, kSmallBytes = 152 * 1024, kSmallRows = 4;   // blocks of 32
@@ -802,6 +824,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
   constexpr int PARTS = SPLIT ? 2 : 1, WAVES = kSmallThreads / 64;
   __shared__ __align__(1024) unsigned char smem[kSmallBytes];
   __shared__ double wave_sums[WAVES];
+  __shared__ float rest[32 * kSmallRows];   // what rounding took off B's diagonal, if not split
   const Job& j = jobs.j[blockIdx.x];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 5, l32 = lane & 31, na = j.na, nx = j.nx;
@@ -929,8 +952,7 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
 
   for (int k = 0; k < steps; ++k) {
     const float a = coefs.c[3 * k], b = coefs.c[3 * k + 1], c = coefs.c[3 * k + 2];
-    const bool in_q = SPLIT || k >= kLoSteps;
-    // A = X X^T, then B = b A + c A A (+ a I); tile (t / na, t % na) is stored transposed
+    // A = X X^T, then B = b A + c A A (+ a I if split); tile (t / na, t % na) is stored transposed
     for (int t = wave; t < na * na; t += WAVES) {
       const int ti = t / na, tj = t % na;
       f16v acc;
@@ -977,13 +999,18 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[e] = b * was[e] + c * (acc[4 * q + e] * kInvScale);
-          if (in_q && ti == tj && l32 == 8 * q + 4 * g + e) v[e] += a * kScale;
+          if (ti == tj && l32 == 8 * q + 4 * g + e) {
+            if constexpr (SPLIT)
+              v[e] += a * kScale;
+            else
+              rest[32 * ti + l32] = v[e] - (float)(_Float16)v[e];
+          }
         }
         put4(four(B + (tj * na + ti) * 2048, q), aplane, SPLIT, v);
       }
     }
     __syncthreads();
-    // X <- a X + B X, or B X: transposed, X^T B, so that a lane has four columns of a row
+    // X <- a X + B X, or B X if split: transposed, X^T B, so that a lane has four columns of a row
     for (int t = wave; t < nx; t += WAVES) {
       f16v acc[kSmallRows];
 #pragma unroll
@@ -1011,11 +1038,11 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(Jobs jobs, Coef
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = acc[i][4 * q + e] * kInvScale;
-          if (!in_q) {
+          if constexpr (!SPLIT) {
             float was[4];
             get4(at, xplane, true, was);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += a * was[e];
+            for (int e = 0; e < 4; ++e) v[e] += (a + rest[32 * i + l32] * kInvScale) * was[e];
           }
           put4(at, xplane, true, v);
         }
@@ -1069,8 +1096,8 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // The tiles.  Square, for A and for all last products too small for the others:
 // three of its workgroups share a CU when the products are rounded, one when
 // they are split.  Small, for B, whose short reduction wants more workgroups: one
-// 1600 x 1600 takes 16 us in 181 of them and 20 us in 91 squares.  Tall and Broad,
-// for last products, read fewer bytes a product.
+// 1600 x 1600 takes 15 us in 181 of them and 20 us in 91 squares (fp16 operands).
+// Tall and Broad, for last products, read fewer bytes a product.
 template <bool SPLIT> using Square = Tile<128, 128, 64, 64, 3, SPLIT ? 1 : 3>;
 template <bool SPLIT> using Small = Tile<64, 128, 32, 64, SPLIT ? 3 : 4, SPLIT ? 2 : 3>;
 using Tall = Tile<320, 256, 160, 64, 4, 2>;
@@ -1080,9 +1107,9 @@ using Broad = Tile<128, 256, 64, 64, 3, 2>;
 // tiles of `area`: the cheapest by a model of a stage's time on a CU, the items
 // on the fullest CU (side by side they take 0.8 of one after the other; split
 // products have no room for two), and the join, which costs a launch and the
-// traffic of every item's sums.  Measured with the join: one 1600 x 6400 weight
-// 33 us in 5 items a tile, 36 in 2, 38 in 3, 35 in 8; two of them 57 us in 2, 63
-// in 1, 55 in 3.
+// traffic of every item's sums.  Measured with the join and fp16 operands: one
+// 1600 x 6400 weight 33 us in 5 items a tile, 36 in 2, 38 in 3, 35 in 8; two of
+// them 57 us in 2, 63 in 1, 55 in 3.
 int splits_for(int64_t tiles, int64_t area, bool split, int stages) {
   const double stage = (split ? 0.75e-6 : 0.3e-6) * (area < 128 * 128 ? 0.6 : 1.0), join = 5e-6, rate = 8e12;
   const int64_t cus = device_cu_count();
@@ -1193,7 +1220,7 @@ unsigned deal(Jobs& jobs, F blocks) {
   return (unsigned)at;
 }
 
-template <int KIND, bool SPLIT, bool LAST, bool ADD, class T>
+template <int KIND, bool SPLIT, bool LAST, class T>
 void product(Jobs& jobs, const Step& st, hipStream_t s) {
   const unsigned grid = deal(jobs, [](const Job& j) {
     if constexpr (KIND == kApply)
@@ -1201,7 +1228,7 @@ void product(Jobs& jobs, const Step& st, hipStream_t s) {
     else
       return up(upper_tiles<T>(j.m) * (KIND == kGram ? j.gram_splits : 1), 8);
   });
-  hipLaunchKernelGGL((ns_product_kernel<KIND, SPLIT, LAST, ADD, T>), dim3(grid), dim3(64 * T::WAVES), 0, s, jobs, st);
+  hipLaunchKernelGGL((ns_product_kernel<KIND, SPLIT, LAST, T>), dim3(grid), dim3(64 * T::WAVES), 0, s, jobs, st);
   if constexpr (KIND == kGram) {
     const unsigned blocks =
         deal(jobs, [](const Job& j) { return j.gram_splits > 1 ? upper_tiles<T>(j.m) * (T::TM * T::TN / 2) : 0; });
@@ -1218,34 +1245,28 @@ int64_t apply_tiles(const Jobs& jobs) {
 
 template <bool SPLIT, class T>
 void apply(Jobs& jobs, const Step& st, bool last, hipStream_t s) {
-  if (last && st.in_q)
-    product<kApply, SPLIT, true, false, T>(jobs, st, s);
-  else if (st.in_q)
-    product<kApply, SPLIT, false, false, T>(jobs, st, s);
-  else if constexpr (!SPLIT) {
-    if (last)
-      product<kApply, SPLIT, true, true, T>(jobs, st, s);
-    else
-      product<kApply, SPLIT, false, true, T>(jobs, st, s);
-  }
+  if (last)
+    product<kApply, SPLIT, true, T>(jobs, st, s);
+  else
+    product<kApply, SPLIT, false, T>(jobs, st, s);
 }
 
 template <bool SPLIT>
 void step(Jobs& jobs, const NsParams& prm, int k, hipStream_t s) {
-  const Step st{k & 1, prm.coef[3 * k], prm.coef[3 * k + 1], prm.coef[3 * k + 2], SPLIT || k >= kLoSteps,
-                SPLIT || k + 1 < kLoSteps};
+  const Step st{k & 1, prm.coef[3 * k], prm.coef[3 * k + 1], prm.coef[3 * k + 2]};
   if (jobs.fine)
-    product<kGram, SPLIT, false, false, Small<SPLIT>>(jobs, st, s);
+    product<kGram, SPLIT, false, Small<SPLIT>>(jobs, st, s);
   else
-    product<kGram, SPLIT, false, false, Square<SPLIT>>(jobs, st, s);
-  product<kPoly, SPLIT, false, false, Small<SPLIT>>(jobs, st, s);
+    product<kGram, SPLIT, false, Square<SPLIT>>(jobs, st, s);
+  product<kPoly, SPLIT, false, Small<SPLIT>>(jobs, st, s);
   const bool last = k + 1 == prm.steps;
   // The larger tile where its whole rounds over the CUs cost less, by area over
-  // measured speed.  Rounded products: two 1600 x 6400 weights take 65 us in 250
-  // Tall tiles and 80 us in 1300 Square ones, one weight 52 and 41 us (the
-  // squares, three to a CU, are taken to fill the CUs evenly).  Split ones: 1024
-  // x 4096 and its transpose take 51 us in 256 Broad tiles, 59 us in 512 Square
-  // ones.
+  // measured speed (the squares of rounded products, three to a CU, are taken to
+  // fill the CUs evenly).  Rounded products, whole calls of five steps: two 1600 x
+  // 6400 weights 852 us with Tall tiles and 895 with Square ones, 4096 x 14336 4.73
+  // and 5.20 ms; the product of one 1600 x 6400 without a X took 52 us in 125 Tall
+  // tiles and 41 in 650 squares.  Split ones: 1024 x 4096 and its transpose take
+  // 51 us in 256 Broad tiles, 59 us in 512 Square ones.
   if (jobs.fine) {
     apply<SPLIT, Small<SPLIT>>(jobs, st, last, s);
     return;
