@@ -501,14 +501,18 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  *
  *   jobs       in    host array: G [R, C] of g_type, out [R, C] of out_type
  *                    (may be G's own memory when the types agree)
- *   coef       in    host array of 3 * steps floats: a, b, c of each step,
- *                    such that no singular value passes 4 on the way
+ *   coef       in    host array of 3 * steps floats: a, b, c of each step.
+ *                    X, A and B must stay within fp16's range: for all s that
+ *                    the steps reach from [0, 1], before a step s^2, in it
+ *                    b s^2 + c s^4 (with a added unless SP24_FP16_OPERANDS)
+ *                    and after the last s have magnitudes up to 15.5
  *   steps            1..SP24_MAX_NS_STEPS
  *   eps              >= 0
  *   workspace        device memory of sp24_orthogonalize_workspace bytes (the
  *                    pointers in jobs do not matter to it)
  * Errors: NULL, SHAPE (also count or steps out of range), ALIGN, LAUNCH;
- * UNSUPPORTED for another type or a negative eps; WORKSPACE; TOO_LARGE when a
+ * UNSUPPORTED for another type, a negative eps or coefficients that leave the
+ * range (checked on the host, before anything is written); WORKSPACE; TOO_LARGE when a
  * job's (min(R, C) + 128) * (max(R, C) + 128) reaches 2^29.
  */
 typedef struct sp24_ortho_job {

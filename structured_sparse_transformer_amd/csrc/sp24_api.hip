@@ -4,6 +4,7 @@
 // then enqueues its kernels on the caller's stream and returns.  Nothing here
 // allocates, frees or synchronises.
 #include <hip/hip_runtime.h>
+#include <cmath>
 #include <cstdint>
 
 #include "sp24.h"
@@ -112,12 +113,41 @@ int check_ns_shape(int64_t R, int64_t C) {
   return R != 0 && C != 0 && R + 128 >= ((int64_t)1 << 29) / (C + 128) ? SP24_ERR_TOO_LARGE : SP24_OK;
 }
 
-int ns_params(const float* coef, int steps, float eps, sp24::NsParams& prm) {
+// Whether X, A and B stay within fp16's range (16 in the units they are held
+// in) for every singular value that the steps can reach from [0, 1].  A matrix's
+// entries are at most its largest singular value, and the steps' polynomials are
+// odd, so [0, s] is followed through them: A has t = s^2, B has b t + c t^2 (and
+// a when `split`), the next X has s (a + b t + c t^2), each largest at an end or
+// where its derivative vanishes.  The last X too: a small weight's stays in LDS.
+bool ns_in_range(const float* coef, int steps, bool split) {
+  constexpr double kMost = 15.5;   // leaves the sums' and roundings' errors room
+  double s = 1.0;
+  for (int k = 0; k < steps; ++k) {
+    const double a = coef[3 * k], b = coef[3 * k + 1], c = coef[3 * k + 2], end = s * s;
+    const auto poly = [&](double t) { return b * t + c * t * t; };
+    double at[5] = {0.0, end, -b / (2.0 * c)};   // B's ends and vertex, then where X's derivative vanishes
+    const double root = std::sqrt(9.0 * b * b - 20.0 * a * c);   // of a + 3 b t + 5 c t^2
+    at[3] = c != 0.0 ? (-3.0 * b + root) / (10.0 * c) : -a / (3.0 * b);
+    at[4] = c != 0.0 ? (-3.0 * b - root) / (10.0 * c) : end;
+    double x = 0.0, most = end;
+    for (const double t : at) {
+      if (!(t >= 0.0 && t <= end)) continue;   // no such point, too
+      most = std::fmax(most, std::fabs((split ? a : 0.0) + poly(t)));
+      x = std::fmax(x, std::sqrt(t) * std::fabs(a + poly(t)));
+    }
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || most > kMost || x > kMost) return false;
+    s = x;
+  }
+  return true;
+}
+
+int ns_params(const float* coef, int steps, float eps, bool split, sp24::NsParams& prm) {
   static_assert(SP24_MAX_NS_STEPS == sp24::kMaxNsSteps && SP24_MAX_BATCH == sp24::kMaxNsJobs, "table sizes");
   if (steps < 1 || steps > SP24_MAX_NS_STEPS) return SP24_ERR_SHAPE;
   if (coef == nullptr) return SP24_ERR_NULL;
-  if (!(eps >= 0.0f)) return SP24_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f) || !ns_in_range(coef, steps, split)) return SP24_ERR_UNSUPPORTED;
   prm.eps = eps;
+  prm.split = split;
   prm.steps = steps;
   for (int k = 0; k < 3 * steps; ++k) prm.coef[k] = coef[k];
   return SP24_OK;
@@ -360,9 +390,8 @@ int sp24_orthogonalize(const sp24_ortho_job* jobs, int count, int g_type, int ou
   if ((g_type != SP24_F16 && g_type != SP24_F32) || (out_type != SP24_F16 && out_type != SP24_F32))
     return SP24_ERR_UNSUPPORTED;
   sp24::NsParams prm{};
-  int st = ns_params(coef, steps, eps, prm);
+  int st = ns_params(coef, steps, eps, !rounded, prm);
   if (st != SP24_OK) return st;
-  prm.split = !rounded;
   sp24::NsJob d[SP24_MAX_BATCH] = {};
   for (int k = 0; k < count; ++k) {
     const sp24_ortho_job& j = jobs[k];
@@ -396,11 +425,10 @@ int sp24_muon_step(const sp24_muon_job* jobs, int count, float momentum, int nes
   if (jobs == nullptr) return SP24_ERR_NULL;
   if (count < 1 || count > SP24_MAX_BATCH) return SP24_ERR_SHAPE;
   sp24::NsParams prm{};
-  int st = ns_params(coef, steps, eps, prm);
+  int st = ns_params(coef, steps, eps, precise != 0, prm);
   if (st != SP24_OK) return st;
   prm.mu = momentum;
   prm.nesterov = nesterov != 0;
-  prm.split = precise != 0;
   sp24::NsJob d[SP24_MAX_BATCH] = {};
   for (int k = 0; k < count; ++k) {
     const sp24_muon_job& j = jobs[k];

@@ -134,3 +134,19 @@ def test_first_step_on_a_low_rank_gradient(sp, precise):
     err = np.linalg.norm(P.cpu().numpy() - (P0.astype(np.float64) - lr * X))
     # and the roundings of P's three operations
     assert err <= bound((256, 400), 5, precise) * lr * np.linalg.norm(X) + 3 * 2.0 ** -24 * (np.linalg.norm(P0) + lr * np.linalg.norm(X))
+
+
+@pytest.mark.parametrize("precise", [True, False])
+@pytest.mark.parametrize("shape", [(1, 1), (40, 70), (300, 400)])
+def test_coefficients_at_the_edge_of_the_range(sp, shape, precise):
+    """A rank-one update's singular value goes 1 -> 3.9 -> -10.9, its square and X itself just inside
+    fp16's range.  Three roundings of 2^-22 (or 2^-12) at most, each times (1 + 2 * 3.8) 3.9 / 10.9 = 3,
+    and the fp32 sums'."""
+    rng = np.random.default_rng([9, *shape])
+    G = (rng.standard_normal((shape[0], 1)) @ rng.standard_normal((1, shape[1]))).astype(np.float32)
+    rows = [(3.9, 0.0, 0.0), (1.0, -0.25, 0.0)]
+    got = sp.sp24_orthogonalize(torch.from_numpy(G).cuda(), 2, rows, dtype=torch.float32, precise=precise)
+    X = float(np.float32(3.9)) * G.astype(np.float64) / (np.linalg.norm(G.astype(np.float64)) + 1e-7)
+    want = X - 0.25 * (X @ X.T @ X)
+    err = np.linalg.norm(got.cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= (1e-5 if precise else 9 * 2.0 ** -12)
