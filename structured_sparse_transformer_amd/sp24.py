@@ -474,14 +474,25 @@ def _workspace(t, need, device):
     return t
 
 
+def _laid_out(ids, stream):
+    """ids as the library takes them.  A part of a token stream may start at any
+    id, and a batch's inputs and targets are views of one tensor: those are copied."""
+    if ids.is_contiguous() and ids.data_ptr() % 16 == 0:
+        return ids
+    with _using(stream):
+        return ids.clone(memory_format=torch.contiguous_format)
+
+
 def sp24_embed_fwd(ids, table, scale=1.0, out=None, stream=None):
     """out [*ids.shape, d] (float16) = scale * table[ids]; rows of ids outside
-    [0, V) are zeros.  ids int32 or int64, table float16 or float32 [V, d]."""
+    [0, V) are zeros.  ids int32 or int64, of any strides; table float16 or
+    float32 [V, d]."""
     types = {torch.float16: F16, torch.float32: F32}
     if table.dtype not in types or table.dim() != 2:
         raise ValueError("the table must be a 2-D float16 or float32 tensor")
     kind = _id_type(ids)
     V, d = table.shape
+    ids = _laid_out(ids, stream)
     with _using(stream):
         out = _out(out, (*ids.shape, d), torch.float16, table.device)
     _check("sp24_embed_fwd", lib().sp24_embed_fwd(_ptr(ids), kind, ids.numel(), _ptr(table), types[table.dtype], V, d,
@@ -505,6 +516,7 @@ def sp24_embed_bwd(ids, dout, V, scale=1.0, dtable=None, accumulate=False, works
     if V < 0:
         raise ValueError("V must not be negative")
     T, d = ids.numel(), dout.shape[-1]
+    ids = _laid_out(ids, stream)
     with _using(stream):
         dtable = _out(dtable, (V, d), torch.float32, dout.device)
         workspace = _workspace(workspace, sp24_embed_bwd_workspace(T, V, d), dout.device)
