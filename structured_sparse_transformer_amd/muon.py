@@ -54,11 +54,25 @@ class Muon:
             self._workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return self._workspace
 
+    def _check(self, grads):
+        """What a call refuses, for all of them before the first: otherwise the
+        weights of earlier calls would have taken the step."""
+        for g, m, p, w in zip(grads, self.momenta, self.masters, self.weights):
+            for t, dtype, name in ((g, torch.float32, "the gradient"), (m, torch.float32, "the momentum"),
+                                   (p, torch.float32, "the weight"), (w, torch.float16, "the float16 weight")):
+                sp24._need(t, p.shape, dtype, name)
+                sp24._ptr(t)
+                if t.data_ptr() % 16:
+                    raise ValueError(f"{name} must be 16-byte aligned")
+
     def step(self, grads) -> None:
         """One step with the gradients of all weights, in their order."""
         if len(grads) != len(self.weights):
             raise ValueError("one gradient per weight")
-        for group in self._groups():
+        groups = self._groups()
+        if len(groups) > 1:
+            self._check(grads)
+        for group in groups:
             sp24.sp24_muon_step(
                 [grads[k] for k in group], [self.momenta[k] for k in group], [self.masters[k] for k in group],
                 [self.weights[k] for k in group],
