@@ -496,6 +496,10 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  * more (3e-3 in five steps), and by up to 3e-3 a step where few roundings
  * average out: with a shorter side, or entries all alike or mostly zero.
  *
+ * The same call gives the same bits.  How the work is dealt out is chosen for
+ * all weights of a call and the GPU's number of CUs, and fp32 sums with it: a
+ * weight's last bits may differ between calls with other weights beside it.
+ *
  * X is held to 2^-36 in absolute terms: an update whose norm is far below eps
  * loses its last bits, and below about 1e-11 eps all of them.
  *
