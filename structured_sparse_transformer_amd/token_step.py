@@ -1,12 +1,13 @@
 """A training step from token ids to new weights: the token embedding, a gated
-2:4-sparse FFN layer (ffn.py) and its optimiser (muon.py), every part in the
-library's kernels.
+2:4-sparse FFN layer (ffn.py) and its optimiser (muon.py), in the library's
+kernels; the table itself takes plain gradient descent, in torch.
 
     X = scale table[ids]                         sp24_embed_fwd
     Y = FFN(X)                                   SparseGegluFFN.forward
     dX, dW1, dW2 from dY                         SparseGegluFFN.backward
     dtable += scale sum over tokens of dX        sp24_embed_bwd
     new W1, W2                                   Muon, then refresh()
+    table -= table_lr dtable, dtable = 0         torch, two passes over the dense table
 
 ``python -m structured_sparse_transformer_amd.token_step`` trains one such
 layer to map tokens to the outputs of a fixed random one and prints its loss.
