@@ -48,9 +48,9 @@
 // in us, with the rate in PFLOP/s and the share of cycles in which the matrix
 // units are busy:
 //                   two parts                        fp16 operands
-//   B X             113 - 116      0.85 - 0.87  0.41   46 - 47       0.70 - 0.71  0.32
+//   B X             113 - 119      0.82 - 0.87  0.41   46 - 47       0.70 - 0.71  0.33
 //   B X of two      189 - 198      0.99 - 1.04  0.53   82 - 86       0.77 - 0.80  0.35
-//   A and its join  58 + 9         0.73         0.43   25 + 8        0.50         0.29
+//   A and its join  58 - 60 + 9    0.71 - 0.73  0.43   25 + 8        0.50         0.29
 //   A^2             25 - 26        0.48         0.19   15            0.27         0.09
 // The matrix instructions alone, without loads or LDS reads, run at 1.56
 // PFLOP/s, the clock down to 1.8 GHz.  What keeps the products from that: the
