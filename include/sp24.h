@@ -486,22 +486,27 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  * they are rounded once at the end.  With the usual coefficients an update of
  * full rank comes within about 1e-5 of exact arithmetic in five steps,
  * normwise.  In directions that an update lacks, a step multiplies rounding
- * errors by a, here as in fp32 arithmetic: any update, of rank one too, comes
- * within 3e-6 a^(steps - 1) (4e-4 in five steps, 2e-2 in eight).
+ * errors by a, here as in fp32 arithmetic: updates of any rank come within
+ * about 3e-6 a^(steps - 1) (4e-4 in five steps, 2e-2 in eight), those whose
+ * entries or rows are all alike, and so are their sums' roundings, within six
+ * times that.
  *
  * With SP24_FP16_OPERANDS added to out_type the products' operands are rounded
  * to fp16 (at a scale that keeps their full precision; X itself keeps two
  * parts), for a third of the matrix work.  A result of either type is then off
  * by up to 6e-4 more a step, normwise, where the update's short side is 128 or
  * more (3e-3 in five steps), and by up to 3e-3 a step where few roundings
- * average out: with a shorter side, or entries all alike or mostly zero.
+ * average out: with a shorter side, or with many entries alike or zero.
  *
  * The same call gives the same bits.  How the work is dealt out is chosen for
  * all weights of a call and the GPU's number of CUs, and fp32 sums with it: a
  * weight's last bits may differ between calls with other weights beside it.
  *
- * X is held to 2^-36 in absolute terms: an update whose norm is far below eps
- * loses its last bits, and below about 1e-11 eps all of them.
+ * X is held to 2^-36 in absolute terms.  Smaller entries of X_0 vanish: an
+ * update whose norm is far below eps loses its last bits, and in the end all.
+ *
+ * The weights of a call are worked on side by side: the buffers of one may not
+ * overlap those of another.
  *
  *   jobs       in    host array: G [R, C] of g_type, out [R, C] of out_type
  *                    (may be G's own memory when the types agree)
@@ -516,8 +521,8 @@ int64_t sp24_embed_bwd_workspace(int64_t T, int64_t V, int64_t d);
  *                    pointers in jobs do not matter to it)
  * Errors: NULL, SHAPE (also count or steps out of range), ALIGN, LAUNCH;
  * UNSUPPORTED for another type, a negative eps or coefficients that leave the
- * range (checked on the host, before anything is written); WORKSPACE; TOO_LARGE when a
- * job's (min(R, C) + 128) * (max(R, C) + 128) reaches 2^29.
+ * range (checked on the host, before anything is written); WORKSPACE;
+ * TOO_LARGE when a job's (min(R, C) + 128) * (max(R, C) + 128) reaches 2^29.
  */
 typedef struct sp24_ortho_job {
   const void* G;
