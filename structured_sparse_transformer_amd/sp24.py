@@ -531,10 +531,13 @@ def _coeffs(coeffs, steps):
     if not 1 <= steps <= MAX_NS_STEPS:
         raise ValueError(f"between 1 and {MAX_NS_STEPS} steps")
     rows = list(NS_COEFFS if coeffs is None else coeffs)
-    rows = [rows] * steps if not hasattr(rows[0], "__len__") else [list(r) for r in rows]
+    try:
+        rows = [[float(v) for v in r] for r in rows]
+    except TypeError:   # numbers, not triples
+        rows = [[float(v) for v in rows]] * steps
     if len(rows) != steps or any(len(r) != 3 for r in rows):
         raise ValueError("coeffs must be (a, b, c), or one such triple per step")
-    return (ctypes.c_float * (3 * steps))(*[float(v) for r in rows for v in r])
+    return (ctypes.c_float * (3 * steps))(*[v for r in rows for v in r])
 
 
 def sp24_orthogonalize_batch(Gs, steps=5, coeffs=None, eps=1e-7, dtype=torch.float16, outs=None, workspace=None,

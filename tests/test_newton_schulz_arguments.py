@@ -104,6 +104,18 @@ def test_random_coefficients_against_a_grid(sp):
     assert min(seen) > 20
 
 
+def test_forms_of_coefficients_that_the_binding_takes(sp):
+    import numpy as np
+    want = [float(ctypes.c_float(v).value) for v in USUAL]
+    for one in (None, USUAL, list(USUAL), np.array(USUAL), torch.tensor(USUAL, dtype=torch.float64)):
+        assert list(sp._coeffs(one, 3)) == want * 3
+    for each in ([USUAL] * 3, np.array([USUAL] * 3), torch.tensor([USUAL] * 3, dtype=torch.float64), iter([USUAL] * 3)):
+        assert list(sp._coeffs(each, 3)) == want * 3
+    for bad in ([], [()], [USUAL] * 2, [USUAL, USUAL, USUAL[:2]], USUAL[:2], np.zeros((0, 3))):
+        with pytest.raises(ValueError):
+            sp._coeffs(bad, 3)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_coefficients_that_are_no_numbers_are_refused(sp, bad):
     for k in range(3):
