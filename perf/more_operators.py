@@ -230,6 +230,10 @@ def prepare(case, seed):
         for k in ("ME", "VE"):
             st[k + "s"] = [st[k][a // 64: -(-(a + n) // 64)] for a, n in zip(_spans(case)[0], sizes)]
     st["lr"], st["seed"] = 1e-3, seed & 0x7FFFFFFF
+    if own:   # the plan of the tensors, which an optimiser keeps
+        from structured_sparse_transformer_amd import sp24
+        eight = {"M_exps": st["MEs"], "V_exps": st["VEs"]} if case["bits"] == 8 else {}
+        st["plan"] = sp24.sp24_adamw_plan(st["Ps"], st["Ms"], st["Vs"], st["Ws"], lrs=st["lr"], decays=st["lr"] * DECAY, **eight)
     return st
 
 
@@ -393,10 +397,7 @@ def _run_own(st):
     if case["op"] == "norm":
         return _control(sp24.sp24_grad_norm(st["Gs"], scale=case["scale"], max_norm=case["max"], control=st["control"]))
     at = {"control": st["control"]} if case["control"] else {"step": case["t"]}
-    if case["bits"] == 8:
-        at.update(M_exps=st["MEs"], V_exps=st["VEs"], seed=st["seed"])
-    sp24.sp24_adamw_step(st["Gs"], st["Ps"], st["Ms"], st["Vs"], st["Ws"], lrs=st["lr"], decays=st["lr"] * DECAY, betas=(B1, B2),
-                         eps=EPS, **at)
+    sp24.sp24_adamw_step(st["plan"], st["Gs"], betas=(B1, B2), eps=EPS, seed=st["seed"], **at)
     out = {"P": st["P"], "W": st["W"]}
     if case["bits"] == 32:
         return {**out, "M": st["M"], "V": st["V"]}
