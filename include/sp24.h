@@ -425,7 +425,9 @@ enum {
   SP24_F16 = 0,
   SP24_F32 = 1,
   SP24_I32 = 2,
-  SP24_I64 = 3
+  SP24_I64 = 3,
+  SP24_BF16 = 4,
+  SP24_STATE8 = 5   /* sp24_adamw_step's states in 8 bits */
 };
 
 /* May be added to sp24_orthogonalize's out_type: products of fp16 operands. */
@@ -577,6 +579,186 @@ int sp24_muon_step(const sp24_muon_job* jobs, int count, float momentum, int nes
 
 /* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
 int64_t sp24_muon_workspace(const sp24_muon_job* jobs, int count);
+
+/* Activations of the products below, act(u) in fp32:
+ *   RELU max(u, 0), RELU2 max(u, 0)^2, GELU u Phi(u), SILU u / (1 + exp(-u)),
+ *   GELU_TANH u/2 (1 + tanh(sqrt(2 / pi) (u + 0.044715 u^3))). */
+enum {
+  SP24_ACT_NONE = 0,
+  SP24_ACT_RELU = 1,
+  SP24_ACT_RELU2 = 2,
+  SP24_ACT_GELU = 3,
+  SP24_ACT_GELU_TANH = 4,
+  SP24_ACT_SILU = 5
+};
+
+/*
+ * Forward 2:4 sparse GEMM of a plain layer with what follows it in the same
+ * pass [Abstract, SW]:
+ *     U = X * Ws^T + bias,   Y = act(U) + residual
+ * fp32 throughout; U (for the backward) and Y are each rounded once, Y from
+ * the unrounded U.  Made for one token as for a training batch.
+ *
+ *   X         in   fp16 [T, C]
+ *   vals_row, meta_row   in   row form of the pruned W [R, C]
+ *   T, R, C        T >= 0; R, C >= 0 and multiples of 16
+ *   bias      in   fp32 [R], or NULL
+ *   act            SP24_ACT_*
+ *   residual  in   fp16 [T, R], or NULL
+ *   U         out  fp16 [T, R], or NULL
+ *   Y         out  fp16 [T, R]; may be the residual's own memory
+ * Infinite U gives what the formulas give in IEEE arithmetic (NaN for -inf with
+ * GELU, GELU_TANH and SILU); NaN gives NaN.
+ * Errors: NULL, SHAPE, ALIGN, LAUNCH; UNSUPPORTED for another act; TOO_LARGE as
+ * for sp24_spmm_fwd, and when R reaches 2^27.
+ */
+int sp24_spmm_fwd_act(const void* X, const void* vals_row, const uint16_t* meta_row, int64_t T, int64_t R, int64_t C,
+                      const float* bias, int act, const void* residual, void* U, void* Y, void* stream);
+
+/*
+ * Input-gradient 2:4 sparse GEMM through the activation before the layer, with
+ * the gradient of that activation's bias [Abstract, SW]:
+ *     dU = (dY * Ws) * act'(U),   dbias[c] = sum over t of dU[t][c]
+ * The layer's input is act(U), U = its predecessor's products with their bias:
+ * dU is the gradient that the predecessor's weight and input gradients take.
+ * RELU's and RELU2's slope at 0 is 0.  fp32 throughout; the sums are of the
+ * unrounded values, in an order that T, R and C fix, so the same call gives
+ * the same bits.
+ *
+ *   dY        in   fp16 [T, R]
+ *   vals_col, meta_col   in   column form of the pruned W [R, C]
+ *   T, R, C        as sp24_spmm_fwd_act
+ *   act            SP24_ACT_*; U may be NULL with SP24_ACT_NONE
+ *   U         in   fp16 [T, C]
+ *   dU        out  fp16 [T, C]; may be U's own memory
+ *   dbias     out  fp32 [C], or NULL.  Written, not accumulated (zeros if T is 0).
+ *   workspace scratch device memory of sp24_spmm_bwd_input_act_workspace bytes
+ *             (NULL where those are 0, or without dbias)
+ * Errors: as sp24_spmm_fwd_act (C reaching 2^27), and WORKSPACE.
+ */
+int sp24_spmm_bwd_input_act(const void* dY, const void* vals_col, const uint16_t* meta_col, int64_t T, int64_t R,
+                            int64_t C, int act, const void* U, void* dU, float* dbias, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_spmm_bwd_input_act_workspace(int64_t T, int64_t R, int64_t C);
+
+/*
+ * Bias gradient of a layer that no activation follows: dbias[r] = sum over t of
+ * dY[t][r], in fp32 in an order that T and R fix.
+ *
+ *   dY        in   fp16 [T, R]
+ *   T, R           >= 0, R a multiple of 16
+ *   dbias     out  fp32 [R], written (zeros if T is 0)
+ *   workspace scratch device memory of sp24_bias_grad_workspace bytes
+ * Errors: NULL, SHAPE, ALIGN, TOO_LARGE, WORKSPACE, LAUNCH.
+ */
+int sp24_bias_grad(const void* dY, int64_t T, int64_t R, float* dbias, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_bias_grad_workspace(int64_t T, int64_t R);
+
+/*
+ * What a training step's optimiser goes by, in device memory, so that no call
+ * waits for the host: sp24_grad_norm writes it, sp24_adamw_step reads it.  All
+ * zeros before the first step.
+ */
+typedef struct sp24_step_control {
+  int64_t step;     /* steps taken, this one included: bias correction's t  */
+  float norm;       /* of the scaled gradients, before clipping             */
+  float factor;     /* what the gradients are multiplied with               */
+  int32_t skip;     /* 1: some gradient is not finite; the step is left out */
+  int32_t unused[3];
+} sp24_step_control;
+
+/*
+ * The norm of all gradients of a step together:
+ *     norm = scale * sqrt(sum of squares),  factor = scale * min(1, max_norm / norm)
+ * into *control.  If some gradient is not finite, skip becomes 1, factor 0 and
+ * step stays; otherwise skip becomes 0 and step grows by 1.  Squares are summed
+ * in fp64, in an order that the sizes fix.
+ *
+ *   grads     in   host array of `count` device pointers, all of g_type
+ *   sizes     in   host array: the number of entries of each, >= 0
+ *   count          >= 0
+ *   g_type         SP24_F16 or SP24_F32
+ *   scale          > 0, finite: what a loss scale left in the gradients is taken off with
+ *   max_norm       > 0; infinity: gradients are not clipped
+ *   control   in/out  one sp24_step_control in device memory
+ *   workspace scratch device memory of sp24_grad_norm_workspace bytes
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, LAUNCH; UNSUPPORTED for another type,
+ * scale or max_norm; TOO_LARGE when a size reaches 2^34.
+ */
+int sp24_grad_norm(const void* const* grads, const int64_t* sizes, int64_t count, int g_type, float scale,
+                   float max_norm, sp24_step_control* control, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_grad_norm_workspace(const int64_t* sizes, int64_t count);
+
+/*
+ * One AdamW step of `count` tensors, in place.  With g = factor * G (factor and
+ * the step t from `control`; 1 and `step` without one):
+ *   M <- beta1 M + (1 - beta1) g,   V <- beta2 V + (1 - beta2) g^2
+ *   P <- (1 - decay) P - lr * (M / (1 - beta1^t)) / (sqrt(V / (1 - beta2^t)) + eps)
+ *   W  = fp16(P)
+ * Where control->skip is set, nothing is written.
+ *
+ * State type SP24_F32: M and V are fp32 [n].  SP24_STATE8: M and V are 8-bit
+ * codes [n] with one exponent byte for every 64 consecutive entries, M_exps and
+ * V_exps [ceil(n / 64)]; all zeros stand for zeros.  An M entry has a sign and
+ * 3 fraction bits, the root of a V entry, which is what is held, 4; both have 4
+ * exponent bits below their group's exponent.  The step uses this step's M and
+ * V before they are rounded; rounded they go up or down at random (unbiased),
+ * by a hash of seed, t, the tensor's place in the call and the entry's in the
+ * tensor, so the same call gives the same bits; a root above zero stays above
+ * zero.  A group in which some entry is not finite turns to NaN.
+ *
+ *   jobs  in  host array, one per tensor:
+ *     G       in      [n] of g_type (SP24_F16 or SP24_F32)
+ *     P       in/out  fp32 [n]
+ *     M, V    in/out  fp32 [n], or codes
+ *     M_exps, V_exps  in/out  uint8 [ceil(n / 64)] (SP24_STATE8; otherwise not read)
+ *     W       out     fp16 [n], or NULL
+ *     n               >= 0
+ *     lr, decay       the update's factor and the part of P that is taken off
+ *                     (lr times the weight decay)
+ *   beta1, beta2      0 <= beta < 1;  eps >= 0
+ *   step              t >= 1 (not read with a control)
+ *   control   in      one sp24_step_control in device memory, or NULL
+ * Pointers are 16-byte aligned, the exponents' at any byte.  The buffers of a
+ * call may not overlap.
+ * Errors: NULL, SHAPE (also step below 1), ALIGN, LAUNCH; UNSUPPORTED for
+ * another type, beta or eps; TOO_LARGE when an n reaches 2^34.
+ */
+typedef struct sp24_adamw_job {
+  const void* G;
+  float* P;
+  void* M;
+  void* V;
+  uint8_t* M_exps;
+  uint8_t* V_exps;
+  void* W;
+  int64_t n;
+  float lr;
+  float decay;
+} sp24_adamw_job;
+
+int sp24_adamw_step(const sp24_adamw_job* jobs, int64_t count, int g_type, int state_type, double beta1, double beta2,
+                    double eps, int64_t step, const sp24_step_control* control, uint32_t seed, void* stream);
+
+/*
+ * The values that an 8-bit state stands for: M's entries, or with root != 0 the
+ * roots of V's.
+ *   codes  in   uint8 [n]     exps  in  uint8 [ceil(n / 64)], at any byte
+ *   n           >= 0
+ *   out    out  [n] of out_type: SP24_F32, or SP24_BF16, which holds such values
+ *               whole unless their group's largest is below 2^-110
+ * Errors: NULL, SHAPE, ALIGN, LAUNCH; UNSUPPORTED for another type; TOO_LARGE
+ * when n reaches 2^34 - 1024.
+ */
+int sp24_state8_values(const uint8_t* codes, const uint8_t* exps, int64_t n, int root, int out_type, void* out,
+                       void* stream);
 
 /* Host only: a static, human-readable name for a status code. */
 const char* sp24_status_str(int status);

@@ -1,0 +1,450 @@
+// The norm of many gradients together, and AdamW over many tensors at once.
+//
+// Tensors go to a launch in a table of kernel arguments, as many as 4 KB hold;
+// a workgroup finds its tensor from its number by the tensors' running counts
+// of chunks.  Every entry is read and written once: both kernels are bound by
+// memory.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "sp24.h"
+#include "sp24_device.hpp"
+#include "sp24_internal.hpp"
+
+namespace sp24 {
+namespace {
+
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+
+// The tensor that chunk c of a launch belongs to: the last whose first chunk
+// is at most c.  Tensors without chunks are not in the table.
+template <int N>
+__device__ __forceinline__ int tensor_of(const uint32_t (&first)[N], int count, uint32_t c) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Four consecutive entries of a tensor as fp32, zeros past its end.
+template <bool kF16>
+__device__ __forceinline__ float4v load4(const void* p, int64_t i, int64_t n) {
+  float4v v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (kF16) {
+    const _Float16* q = static_cast<const _Float16*>(p) + i;
+    if (i + 4 <= n) {
+      const half4 x = *reinterpret_cast<const half4*>(q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = (float)x[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < n) v[e] = (float)q[e];
+    }
+  } else {
+    const float* q = static_cast<const float*>(p) + i;
+    if (i + 4 <= n) return *reinterpret_cast<const float4v*>(q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < n) v[e] = q[e];
+  }
+  return v;
+}
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, float4v v) {
+  if (i + 4 <= n) {
+    *reinterpret_cast<float4v*>(p + i) = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) p[i + e] = v[e];
+}
+
+// ---------------------------------------------------------------------------
+// The norm.  Squares are summed in fp64: no finite gradients overflow, and the
+// sum is not finite only where an entry is not.
+
+constexpr int kNormTensors = 128;
+constexpr int64_t kNormChunk = 16384;
+struct NormTable {
+  const void* g[kNormTensors];
+  int64_t n[kNormTensors];
+  uint32_t first[kNormTensors];
+  int count;
+};
+static_assert(sizeof(NormTable) <= 3800, "kernel arguments");
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int x = 32; x >= 1; x /= 2) v += __shfl_xor(v, x);
+  return v;
+}
+
+template <bool kF16>
+__global__ __launch_bounds__(kThreads) void squares_kernel(NormTable tab, double* __restrict__ part) {
+  __shared__ double waves[kThreads / 64];
+  const int k = tensor_of(tab.first, tab.count, blockIdx.x);
+  const int64_t n = tab.n[k], i0 = (int64_t)(blockIdx.x - tab.first[k]) * kNormChunk;
+  double sum = 0.0;
+  for (int u = 0; u < kNormChunk / (4 * kThreads); ++u) {
+    const int64_t i = i0 + (u * kThreads + (int)threadIdx.x) * 4;
+    if (i >= n) break;
+    const float4v x = load4<kF16>(tab.g[k], i, n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
+  }
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = waves[0] + waves[1] + (waves[2] + waves[3]);
+}
+
+typedef sp24_step_control Control;
+
+__global__ __launch_bounds__(1024) void norm_kernel(const double* __restrict__ part, int64_t parts, double scale,
+                                                    double max_norm, Control* control) {
+  __shared__ double waves[16];
+  double sum = 0.0;
+  for (int64_t p = threadIdx.x; p < parts; p += 1024) sum += part[p];
+  sum = wave_sum(sum);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  sum = 0.0;
+  for (int w = 0; w < 16; ++w) sum += waves[w];
+  const double norm = __builtin_sqrt(sum) * scale;
+  const bool fine = __builtin_isfinite(norm);
+  control->norm = (float)norm;
+  control->factor = fine ? (float)(norm > max_norm ? scale * (max_norm / norm) : scale) : 0.0f;
+  control->skip = !fine;
+  if (fine) control->step += 1;
+}
+
+// ---------------------------------------------------------------------------
+// States in 8 bits.
+//
+// Groups of 64 consecutive entries share an exponent E (that of the fp32
+// format, 0..254; 255: some entry of the group is not finite).  A magnitude
+// has 4 exponent and F fraction bits: M's F = 3 and a sign, the root of V's
+// F = 4.  With e and f its exponent and fraction fields it stands for
+//   (e ? 1 + f / 2^F : f / 2^F) 2^(E - 127 - 15 + max(e, 1)),
+// that is, for the fp32 number of bits code << (23 - F) times 2^(E - 15): the
+// small magnitudes fall on fp32's own subnormals, and encoding is a scaling by
+// a power of two and a rounding of the bits.
+//
+// V is held as its root, for half the range, and both are rounded up or down
+// at random: with b2 = 0.999 a step moves a root by a 2000th, which rounding to
+// nearest among steps of a 32nd would drop for ever.  A root above zero stays
+// above zero, so that no entry's step is divided by eps alone.
+
+constexpr int kFracM = 3, kFracV = 4;
+
+template <int F>
+__device__ __forceinline__ float held_value(uint32_t magnitude, int E) {
+  const float x = __builtin_amdgcn_ldexpf(__builtin_bit_cast(float, magnitude << (23 - F)), E - 15);
+  return E == 255 ? __builtin_nanf("") : x;
+}
+
+// The exponent for a group whose largest magnitude has these bits: that of the
+// magnitude rounded up to F fraction bits, so that no rounding leaves the format.
+template <int F>
+__device__ __forceinline__ int group_exponent(uint32_t top) {
+  const uint32_t E = (top + ((1u << (23 - F)) - 1)) >> 23;
+  return top >= 0x7F800000u ? 255 : (int)min(E, 254u);
+}
+
+__device__ __forceinline__ uint32_t magnitude_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu; }
+
+// x >= 0 (finite) rounded up where the bits that the code drops and 16 random
+// ones carry.
+template <int F>
+__device__ __forceinline__ uint32_t held_code(float x, int E, uint32_t random16) {
+  constexpr int kDrop = 23 - F;
+  const uint32_t y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_ldexpf(x, 15 - E));
+  const uint32_t code = (y + (random16 << (kDrop - 16)) + (1u << (kDrop - 17))) >> kDrop;
+  return min(code, (1u << (4 + F)) - 1);
+}
+
+// 32 bits mixed by multiplications with the first bits of the roots of 2 and 3.
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x6A09E667u;
+  x = (x ^ (x >> 15)) * 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+// ---------------------------------------------------------------------------
+// AdamW.
+
+constexpr int kAdamTensors = 40;
+constexpr int64_t kAdamChunk = 4096;
+struct AdamEntry {
+  const void* G;
+  float* P;
+  void* M;
+  void* V;
+  uint8_t* ME;
+  uint8_t* VE;
+  uint16_t* W;
+  int64_t n;
+  float lr, keep;
+  uint32_t place;
+};
+struct AdamTable {
+  AdamEntry t[kAdamTensors];
+  uint32_t first[kAdamTensors];
+  int count;
+  float b1, c1, b2, c2, eps, ln_b1, ln_b2;
+  int64_t step;
+  const Control* control;
+  uint32_t seed;
+};
+static_assert(sizeof(AdamTable) <= 4000, "kernel arguments");
+
+template <bool kF16, bool k8>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable tab) {
+  int64_t step = tab.step;
+  float factor = 1.0f;
+  if (tab.control != nullptr) {
+    if (tab.control->skip != 0) return;
+    step = tab.control->step;
+    factor = tab.control->factor;
+  }
+  const int k = tensor_of(tab.first, tab.count, blockIdx.x);
+  const AdamEntry& t = tab.t[k];
+  const int64_t n = t.n, i0 = (int64_t)(blockIdx.x - tab.first[k]) * kAdamChunk;
+  // 1 - b^step through expm1: the difference keeps its precision for b near 1
+  const float rate = t.lr / -expm1f((float)step * tab.ln_b1);
+  const float root = 1.0f / sqrtf(-expm1f((float)step * tab.ln_b2));
+  const uint32_t key = mix(mix(mix((uint32_t)step) ^ tab.seed) ^ t.place);
+  for (int u = 0; u < kAdamChunk / (4 * kThreads); ++u) {
+    const int64_t i = i0 + (u * kThreads + (int)threadIdx.x) * 4;
+    if (i0 + u * kThreads * 4 >= n) break;   // the whole workgroup: groups of lanes exchange values below
+    const float4v g = load4<kF16>(t.G, i, n);
+    float4v p = load4<false>(t.P, i, n), m, v, r;
+    if constexpr (k8) {
+      const bool in = i < n;
+      const int64_t j = in ? i : 0;
+      uint32_t mc = 0, vc = 0;
+      if (i + 4 <= n) {
+        mc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.M) + i);
+        vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.V) + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < n) {
+            mc |= (uint32_t)static_cast<const uint8_t*>(t.M)[i + e] << (8 * e);
+            vc |= (uint32_t)static_cast<const uint8_t*>(t.V)[i + e] << (8 * e);
+          }
+      }
+      const int me = t.ME[j / 64], ve = t.VE[j / 64];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a = mc >> (8 * e) & 255, b = vc >> (8 * e) & 255;
+        const float x = held_value<kFracM>(a & 127, me);
+        m[e] = a & 128 ? -x : x;
+        r[e] = held_value<kFracV>(b, ve);
+        v[e] = r[e] * r[e];
+      }
+    } else {
+      m = load4<false>(t.M, i, n);
+      v = load4<false>(t.V, i, n);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = g[e] * factor;
+      m[e] = m[e] * tab.b1 + x * tab.c1;
+      v[e] = v[e] * tab.b2 + x * x * tab.c2;
+      r[e] = sqrtf(v[e]);
+      p[e] = p[e] * t.keep - rate * m[e] / (r[e] * root + tab.eps);
+    }
+    store4(t.P, i, n, p);
+    if (t.W != nullptr) {
+      if (i + 4 <= n) {
+        *reinterpret_cast<half4*>(t.W + i) = half4{(_Float16)p[0], (_Float16)p[1], (_Float16)p[2], (_Float16)p[3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < n) t.W[i + e] = __builtin_bit_cast(uint16_t, (_Float16)p[e]);
+      }
+    }
+    if constexpr (k8) {
+      // 16 lanes hold a group.  Lanes past the end hold zeros.
+      uint32_t tm = 0, tv = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i + e >= n) m[e] = r[e] = 0.0f;
+        tm = max(tm, magnitude_bits(m[e]));
+        tv = max(tv, magnitude_bits(r[e]));
+      }
+#pragma unroll
+      for (int x = 1; x < 16; x *= 2) {
+        tm = max(tm, (uint32_t)__shfl_xor((int)tm, x));
+        tv = max(tv, (uint32_t)__shfl_xor((int)tv, x));
+      }
+      const int me = group_exponent<kFracM>(tm), ve = group_exponent<kFracV>(tv);
+      uint32_t mc = 0, vc = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t h = mix((uint32_t)(i + e) ^ key);
+        uint32_t a = me == 255 ? 0 : held_code<kFracM>(__builtin_fabsf(m[e]), me, h & 0xFFFFu);
+        uint32_t b = ve == 255 ? 0 : held_code<kFracV>(r[e], ve, h >> 16);
+        if (m[e] < 0.0f) a |= 128;
+        if (r[e] > 0.0f && b == 0) b = 1;
+        mc |= a << (8 * e);
+        vc |= b << (8 * e);
+      }
+      if (i + 4 <= n) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.M) + i) = mc;
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.V) + i) = vc;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < n) {
+            static_cast<uint8_t*>(t.M)[i + e] = (uint8_t)(mc >> (8 * e));
+            static_cast<uint8_t*>(t.V)[i + e] = (uint8_t)(vc >> (8 * e));
+          }
+      }
+      if ((threadIdx.x & 15) == 0 && i < n) {
+        t.ME[i / 64] = (uint8_t)me;
+        t.VE[i / 64] = (uint8_t)ve;
+      }
+    } else {
+      store4(static_cast<float*>(t.M), i, n, m);
+      store4(static_cast<float*>(t.V), i, n, v);
+    }
+  }
+}
+
+// What a state of 8 bits stands for.
+template <bool kRoot, bool kBf16>
+__global__ __launch_bounds__(kThreads) void state8_values_kernel(const uint8_t* __restrict__ codes,
+                                                                 const uint8_t* __restrict__ exps, int64_t n,
+                                                                 void* __restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int E = exps[i / 64];
+  float x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t c = i + e < n ? codes[i + e] : 0;
+    x[e] = kRoot ? held_value<kFracV>(c, E) : held_value<kFracM>(c & 127, E);
+    if (!kRoot && c & 128) x[e] = -x[e];
+  }
+  if constexpr (kBf16) {
+    // five significant bits at most: the upper half holds them all
+    uint16_t* o = static_cast<uint16_t*>(out) + i;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < n) o[e] = (uint16_t)(__builtin_bit_cast(uint32_t, x[e]) >> 16);
+  } else {
+    store4(static_cast<float*>(out), i, n, float4v{x[0], x[1], x[2], x[3]});
+  }
+}
+
+int64_t chunks_of(int64_t n, int64_t chunk) { return (n + chunk - 1) / chunk; }
+
+}  // namespace
+
+int64_t grad_norm_workspace(const int64_t* sizes, int64_t count) {
+  int64_t parts = 0;
+  for (int64_t k = 0; k < count; ++k) parts += chunks_of(sizes[k], kNormChunk);
+  return parts * (int64_t)sizeof(double);
+}
+
+hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, int64_t count, bool f16, double scale,
+                            double max_norm, void* control, void* ws, hipStream_t s) {
+  double* const part = static_cast<double*>(ws);
+  int64_t parts = 0;
+  NormTable tab;
+  tab.count = 0;
+  uint32_t chunks = 0;
+  const auto flush = [&]() {
+    if (tab.count == 0) return hipSuccess;
+    const dim3 grid(chunks), block(kThreads);
+    if (f16) hipLaunchKernelGGL(squares_kernel<true>, grid, block, 0, s, tab, part + parts);
+    else hipLaunchKernelGGL(squares_kernel<false>, grid, block, 0, s, tab, part + parts);
+    parts += chunks;
+    tab.count = 0;
+    chunks = 0;
+    return hipGetLastError();
+  };
+  for (int64_t k = 0; k < count; ++k) {
+    const int64_t c = chunks_of(sizes[k], kNormChunk);
+    if (c == 0) continue;
+    if (tab.count == kNormTensors || chunks + c > kMaxGrid) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    tab.g[tab.count] = grads[k];
+    tab.n[tab.count] = sizes[k];
+    tab.first[tab.count++] = chunks;
+    chunks += (uint32_t)c;
+  }
+  const hipError_t e = flush();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(1024), 0, s, part, parts, scale, max_norm, static_cast<Control*>(control));
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, bool state8, const AdamwParams& prm, hipStream_t s) {
+  AdamTable tab;
+  tab.b1 = (float)prm.beta1;
+  tab.c1 = (float)(1.0 - prm.beta1);
+  tab.b2 = (float)prm.beta2;
+  tab.c2 = (float)(1.0 - prm.beta2);
+  tab.eps = (float)prm.eps;
+  tab.ln_b1 = (float)std::log(prm.beta1);
+  tab.ln_b2 = (float)std::log(prm.beta2);
+  tab.step = prm.step;
+  tab.control = static_cast<const Control*>(prm.control);
+  tab.seed = prm.seed;
+  tab.count = 0;
+  uint32_t chunks = 0;
+  const auto flush = [&]() {
+    if (tab.count == 0) return hipSuccess;
+    const dim3 grid(chunks), block(kThreads);
+    if (f16 && state8) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, s, tab);
+    else if (f16) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, s, tab);
+    else if (state8) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, s, tab);
+    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, s, tab);
+    tab.count = 0;
+    chunks = 0;
+    return hipGetLastError();
+  };
+  for (int64_t k = 0; k < count; ++k) {
+    const sp24_adamw_job& j = jobs[k];
+    const int64_t c = chunks_of(j.n, kAdamChunk);
+    if (c == 0) continue;
+    if (tab.count == kAdamTensors || chunks + c > kMaxGrid) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    tab.t[tab.count] = AdamEntry{j.G, j.P, j.M, j.V, j.M_exps, j.V_exps, static_cast<uint16_t*>(j.W),
+                                  j.n, j.lr, 1.0f - j.decay, (uint32_t)k};
+    tab.first[tab.count++] = chunks;
+    chunks += (uint32_t)c;
+  }
+  return flush();
+}
+
+hipError_t launch_state8_values(const uint8_t* codes, const uint8_t* exps, int64_t n, bool root, bool bf16, void* out,
+                                hipStream_t s) {
+  if (n == 0) return hipSuccess;
+  const dim3 grid((unsigned)chunks_of(n, 4 * kThreads)), block(kThreads);
+  if (root && bf16) hipLaunchKernelGGL((state8_values_kernel<true, true>), grid, block, 0, s, codes, exps, n, out);
+  else if (root) hipLaunchKernelGGL((state8_values_kernel<true, false>), grid, block, 0, s, codes, exps, n, out);
+  else if (bf16) hipLaunchKernelGGL((state8_values_kernel<false, true>), grid, block, 0, s, codes, exps, n, out);
+  else hipLaunchKernelGGL((state8_values_kernel<false, false>), grid, block, 0, s, codes, exps, n, out);
+  return hipGetLastError();
+}
+
+}  // namespace sp24

@@ -164,6 +164,44 @@ int ns_launch(const sp24::NsJob* d, int count, const sp24::NsParams& prm, void* 
   return launch_status(sp24::launch_newton_schulz(d, count, prm, workspace, as_stream(stream)));
 }
 
+// The products with an epilogue launch a workgroup of 512 for 16 features.
+constexpr int64_t kMaxActFeatures = (int64_t)1 << 27;
+
+int check_spmm_act(const void* A, const void* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K, int act,
+                   const void* out) {
+  if (act < 0 || act >= sp24::kActCount) return SP24_ERR_UNSUPPORTED;
+  const int st = check_spmm(A, vals, meta, T, N, K, out);
+  return st == SP24_OK && N >= kMaxActFeatures ? SP24_ERR_TOO_LARGE : st;
+}
+
+// A call's workspace of `need` bytes.
+int check_workspace(const void* workspace, int64_t workspace_bytes, int64_t need) {
+  if (need == 0) return SP24_OK;
+  if (workspace == nullptr) return SP24_ERR_NULL;
+  if (!aligned16(workspace)) return SP24_ERR_ALIGN;
+  return workspace_bytes < need ? SP24_ERR_WORKSPACE : SP24_OK;
+}
+
+int check_bias_grad(int64_t T, int64_t R) {
+  if (T < 0) return SP24_ERR_SHAPE;
+  const int st = check_dims(R, 0, 16);
+  if (st != SP24_OK) return st;
+  return T >= kMaxDim || (T != 0 && R >= kMaxElems / T) ? SP24_ERR_TOO_LARGE : SP24_OK;
+}
+
+// Entries of a tensor of the optimiser's calls: at most 2^22 chunks of 4096.
+constexpr int64_t kMaxEntries = (int64_t)1 << 34;
+
+int check_sizes(const int64_t* sizes, int64_t count) {
+  if (count < 0) return SP24_ERR_SHAPE;
+  if (count != 0 && sizes == nullptr) return SP24_ERR_NULL;
+  for (int64_t k = 0; k < count; ++k) {
+    if (sizes[k] < 0) return SP24_ERR_SHAPE;
+    if (sizes[k] >= kMaxEntries) return SP24_ERR_TOO_LARGE;
+  }
+  return SP24_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -447,6 +485,113 @@ int sp24_muon_step(const sp24_muon_job* jobs, int count, float momentum, int nes
     d[k].keep = 1.0f - j.decay;
   }
   return ns_launch(d, count, prm, workspace, workspace_bytes, stream);
+}
+
+int sp24_spmm_fwd_act(const void* X, const void* vals_row, const uint16_t* meta_row, int64_t T, int64_t R, int64_t C,
+                      const float* bias, int act, const void* residual, void* U, void* Y, void* stream) {
+  static_assert((int)SP24_ACT_SILU == (int)sp24::kActSilu && (int)SP24_ACT_GELU == (int)sp24::kActGelu, "activations");
+  const int st = check_spmm_act(X, vals_row, meta_row, T, R, C, act, Y);
+  if (st != SP24_OK || T == 0 || R == 0) return st;
+  if ((bias && !aligned16(bias)) || (residual && !aligned16(residual)) || (U && !aligned16(U))) return SP24_ERR_ALIGN;
+  return launch_status(sp24::launch_spmm_act_fwd(
+      static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(vals_row), meta_row, T, R, C, bias, act,
+      static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(U), static_cast<uint16_t*>(Y), as_stream(stream)));
+}
+
+int64_t sp24_spmm_bwd_input_act_workspace(int64_t T, int64_t R, int64_t C) {
+  // sizes alone: no pointer is looked at with T = 0
+  if (check_spmm(nullptr, nullptr, nullptr, 0, C, R, nullptr) != SP24_OK || C >= kMaxActFeatures || T < 0 ||
+      T >= kMaxDim || (T != 0 && (R >= kMaxElems / T || C >= kMaxElems / T)))
+    return -1;
+  return sp24::spmm_act_bwd_workspace(T, C);
+}
+
+int sp24_spmm_bwd_input_act(const void* dY, const void* vals_col, const uint16_t* meta_col, int64_t T, int64_t R,
+                            int64_t C, int act, const void* U, void* dU, float* dbias, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  int st = check_spmm_act(dY, vals_col, meta_col, T, C, R, act, dU);
+  if (st != SP24_OK || C == 0) return st;
+  if (dbias && !aligned16(dbias)) return SP24_ERR_ALIGN;
+  if (T != 0) {
+    if (act != SP24_ACT_NONE && U == nullptr) return SP24_ERR_NULL;
+    if (U && !aligned16(U)) return SP24_ERR_ALIGN;
+    if (dbias && (st = check_workspace(workspace, workspace_bytes, sp24::spmm_act_bwd_workspace(T, C))) != SP24_OK)
+      return st;
+  }
+  return launch_status(sp24::launch_spmm_act_bwd(static_cast<const uint16_t*>(dY), static_cast<const uint16_t*>(vals_col),
+                                                 meta_col, T, C, R, act, static_cast<const uint16_t*>(U),
+                                                 static_cast<uint16_t*>(dU), dbias, workspace, as_stream(stream)));
+}
+
+int64_t sp24_bias_grad_workspace(int64_t T, int64_t R) {
+  return check_bias_grad(T, R) == SP24_OK ? sp24::bias_grad_workspace(T, R) : -1;
+}
+
+int sp24_bias_grad(const void* dY, int64_t T, int64_t R, float* dbias, void* workspace, int64_t workspace_bytes,
+                   void* stream) {
+  int st = check_bias_grad(T, R);
+  if (st != SP24_OK || R == 0) return st;
+  if (dbias == nullptr || (T != 0 && dY == nullptr)) return SP24_ERR_NULL;
+  if (!aligned16(dbias) || (T != 0 && !aligned16(dY))) return SP24_ERR_ALIGN;
+  if ((st = check_workspace(workspace, workspace_bytes, sp24::bias_grad_workspace(T, R))) != SP24_OK) return st;
+  return launch_status(
+      sp24::launch_bias_grad(static_cast<const uint16_t*>(dY), T, R, dbias, workspace, as_stream(stream)));
+}
+
+int64_t sp24_grad_norm_workspace(const int64_t* sizes, int64_t count) {
+  return check_sizes(sizes, count) == SP24_OK ? sp24::grad_norm_workspace(sizes, count) : -1;
+}
+
+int sp24_grad_norm(const void* const* grads, const int64_t* sizes, int64_t count, int g_type, float scale,
+                   float max_norm, sp24_step_control* control, void* workspace, int64_t workspace_bytes, void* stream) {
+  if ((g_type != SP24_F16 && g_type != SP24_F32) || !(scale > 0.0f) || !std::isfinite(scale) || !(max_norm > 0.0f))
+    return SP24_ERR_UNSUPPORTED;
+  int st = check_sizes(sizes, count);
+  if (st != SP24_OK) return st;
+  if (control == nullptr || (count != 0 && grads == nullptr)) return SP24_ERR_NULL;
+  for (int64_t k = 0; k < count; ++k)
+    if (sizes[k] != 0 && grads[k] == nullptr) return SP24_ERR_NULL;
+  if (!aligned16(control)) return SP24_ERR_ALIGN;
+  for (int64_t k = 0; k < count; ++k)
+    if (sizes[k] != 0 && !aligned16(grads[k])) return SP24_ERR_ALIGN;
+  if ((st = check_workspace(workspace, workspace_bytes, sp24::grad_norm_workspace(sizes, count))) != SP24_OK) return st;
+  return launch_status(sp24::launch_grad_norm(grads, sizes, count, g_type == SP24_F16, scale, max_norm, control,
+                                              workspace, as_stream(stream)));
+}
+
+int sp24_adamw_step(const sp24_adamw_job* jobs, int64_t count, int g_type, int state_type, double beta1, double beta2,
+                    double eps, int64_t step, const sp24_step_control* control, uint32_t seed, void* stream) {
+  if (count < 0) return SP24_ERR_SHAPE;
+  if (count != 0 && jobs == nullptr) return SP24_ERR_NULL;
+  if ((g_type != SP24_F16 && g_type != SP24_F32) || (state_type != SP24_F32 && state_type != SP24_STATE8) ||
+      !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0))
+    return SP24_ERR_UNSUPPORTED;
+  if (control == nullptr && step < 1) return SP24_ERR_SHAPE;
+  if (control && !aligned16(control)) return SP24_ERR_ALIGN;
+  const bool state8 = state_type == SP24_STATE8;
+  for (int64_t k = 0; k < count; ++k) {
+    const sp24_adamw_job& j = jobs[k];
+    if (j.n < 0) return SP24_ERR_SHAPE;
+    if (j.n >= kMaxEntries) return SP24_ERR_TOO_LARGE;
+    if (j.n == 0) continue;
+    if (!j.G || !j.P || !j.M || !j.V || (state8 && (!j.M_exps || !j.V_exps))) return SP24_ERR_NULL;
+    if (!aligned16(j.G) || !aligned16(j.P) || !aligned16(j.M) || !aligned16(j.V) || (j.W && !aligned16(j.W)))
+      return SP24_ERR_ALIGN;
+  }
+  return launch_status(sp24::launch_adamw(jobs, count, g_type == SP24_F16, state8,
+                                          {beta1, beta2, eps, step, control, seed}, as_stream(stream)));
+}
+
+int sp24_state8_values(const uint8_t* codes, const uint8_t* exps, int64_t n, int root, int out_type, void* out,
+                       void* stream) {
+  if (out_type != SP24_F32 && out_type != SP24_BF16) return SP24_ERR_UNSUPPORTED;
+  if (n < 0) return SP24_ERR_SHAPE;
+  if (n >= kMaxEntries - 1024) return SP24_ERR_TOO_LARGE;
+  if (n == 0) return SP24_OK;
+  if (codes == nullptr || exps == nullptr || out == nullptr) return SP24_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(out)) return SP24_ERR_ALIGN;
+  return launch_status(
+      sp24::launch_state8_values(codes, exps, n, root != 0, out_type == SP24_BF16, out, as_stream(stream)));
 }
 
 const char* sp24_status_str(int status) {

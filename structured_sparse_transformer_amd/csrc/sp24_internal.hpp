@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
+struct sp24_adamw_job;   // sp24.h
+
 namespace sp24 {
 
 // Element offset of (r, c) in an n x m matrix stored in the compressed forms'
@@ -142,5 +144,43 @@ struct NsParams {
 // Workspace bytes of a launch over these jobs (their R and C alone matter).
 int64_t ns_workspace(const NsJob* jobs, int count);
 hipError_t launch_newton_schulz(const NsJob* jobs, int count, const NsParams& prm, void* ws, hipStream_t s);
+
+// Activations of the products with an epilogue (SP24_ACT_* of sp24.h).
+enum { kActNone = 0, kActRelu, kActRelu2, kActGelu, kActGeluTanh, kActSilu, kActCount };
+
+// U = X S^T + bias, Y = act(U) + residual; bias, residual and U may be null.
+// X [T][K], S's forms as launch_spmm_nt takes them, the others [T][N].
+hipError_t launch_spmm_act_fwd(const uint16_t* X, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N,
+                               int64_t K, const float* bias, int act, const uint16_t* residual, uint16_t* U,
+                               uint16_t* Y, hipStream_t s);
+// dU = (dY S^T) * act'(U) and, unless dbias is null, its sums over tokens.  ws:
+// spmm_act_bwd_workspace bytes (none needed without dbias).
+int64_t spmm_act_bwd_workspace(int64_t T, int64_t N);
+hipError_t launch_spmm_act_bwd(const uint16_t* dY, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N,
+                               int64_t K, int act, const uint16_t* U, uint16_t* dU, float* dbias, void* ws,
+                               hipStream_t s);
+// out[R] = the sums of dY [T][R] over tokens; R a multiple of 16.
+int64_t bias_grad_workspace(int64_t T, int64_t R);
+hipError_t launch_bias_grad(const uint16_t* dY, int64_t T, int64_t R, float* out, void* ws, hipStream_t s);
+
+// Workgroups of 256 in one launch: HIP counts a grid's work-items in 32 bits.
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
+
+// The gradients' norm into a control block (sp24_step_control).
+int64_t grad_norm_workspace(const int64_t* sizes, int64_t count);
+hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, int64_t count, bool f16, double scale,
+                            double max_norm, void* control, void* ws, hipStream_t s);
+
+// An AdamW step over the C ABI's jobs, checked.
+struct AdamwParams {
+  double beta1, beta2, eps;
+  int64_t step;
+  const void* control;   // or null: step counts, and gradients are taken whole
+  uint32_t seed;
+};
+hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, bool state8, const AdamwParams& prm, hipStream_t s);
+// The values that 8-bit codes stand for: M's, or the roots of V's.
+hipError_t launch_state8_values(const uint8_t* codes, const uint8_t* exps, int64_t n, bool root, bool bf16, void* out,
+                                hipStream_t s);
 
 }  // namespace sp24

@@ -33,13 +33,18 @@ EXPORTS = ("sp24_mask_search", "sp24_compress", "sp24_search_compress", "sp24_se
            "sp24_spmm_fwd", "sp24_spmm_fwd_geglu", "sp24_spmm_bwd_input", "sp24_spmm_group",
            "sp24_spmm_group_noalloc", "sp24_embed_fwd", "sp24_embed_bwd", "sp24_embed_bwd_workspace",
            "sp24_orthogonalize", "sp24_orthogonalize_workspace", "sp24_muon_step", "sp24_muon_workspace",
+           "sp24_spmm_fwd_act", "sp24_spmm_bwd_input_act", "sp24_spmm_bwd_input_act_workspace",
+           "sp24_bias_grad", "sp24_bias_grad_workspace", "sp24_grad_norm", "sp24_grad_norm_workspace",
+           "sp24_adamw_step", "sp24_state8_values",
            "sp24_status_str",
            "sp24_pattern_table", "sp24_abi_version")
 MAX_BATCH = 8
 MAX_GROUP = 8
 GROUP_WORKSPACE_BYTES = 64
 MAX_NS_STEPS = 32
-F16, F32, I32, I64 = 0, 1, 2, 3
+F16, F32, I32, I64, BF16, STATE8 = 0, 1, 2, 3, 4, 5
+# SP24_ACT_*, by name
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 FP16_OPERANDS = 16
 # the usual quintic of the Newton-Schulz iteration: five steps bring singular
 # values to about [0.7, 1.2]
@@ -69,6 +74,13 @@ class MuonJob(ctypes.Structure):
     """Mirror of sp24_muon_job (include/sp24.h)."""
     _fields_ = [("G", ctypes.c_void_p), ("M", ctypes.c_void_p), ("P", ctypes.c_void_p), ("W", ctypes.c_void_p),
                 ("R", ctypes.c_int64), ("C", ctypes.c_int64), ("lr", ctypes.c_float), ("decay", ctypes.c_float)]
+
+
+class AdamwJob(ctypes.Structure):
+    """Mirror of sp24_adamw_job (include/sp24.h)."""
+    _fields_ = [("G", ctypes.c_void_p), ("P", ctypes.c_void_p), ("M", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("M_exps", ctypes.c_void_p), ("V_exps", ctypes.c_void_p), ("W", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("lr", ctypes.c_float), ("decay", ctypes.c_float)]
 
 
 class Sp24Error(RuntimeError):
@@ -110,6 +122,16 @@ def lib() -> ctypes.CDLL:
             "sp24_orthogonalize_workspace": [p, i32],
             "sp24_muon_step": [p, i32, ctypes.c_float, i32, i32, p, i32, ctypes.c_float, p, i64, p],
             "sp24_muon_workspace": [p, i32],
+            "sp24_spmm_fwd_act": [p, p, p, i64, i64, i64, p, i32, p, p, p, p],
+            "sp24_spmm_bwd_input_act": [p, p, p, i64, i64, i64, i32, p, p, p, p, i64, p],
+            "sp24_spmm_bwd_input_act_workspace": [i64, i64, i64],
+            "sp24_bias_grad": [p, i64, i64, p, p, i64, p],
+            "sp24_bias_grad_workspace": [i64, i64],
+            "sp24_grad_norm": [p, p, i64, i32, ctypes.c_float, ctypes.c_float, p, p, i64, p],
+            "sp24_grad_norm_workspace": [p, i64],
+            "sp24_adamw_step": [p, i64, i32, i32, ctypes.c_double, ctypes.c_double, ctypes.c_double, i64, p,
+                                ctypes.c_uint32, p],
+            "sp24_state8_values": [p, p, i64, i32, i32, p, p],
             "sp24_status_str": [i32],
             "sp24_pattern_table": [p],
             "sp24_abi_version": [],
@@ -609,3 +631,212 @@ def sp24_muon_step(Gs, Ms, Ps, Ws, lrs, decays=None, momentum=0.95, nesterov=Tru
     _check("sp24_muon_step", lib().sp24_muon_step(
         arr, n, float(momentum), int(bool(nesterov)), int(bool(precise)), ctypes.cast(coef, ctypes.c_void_p), steps,
         float(eps), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _act(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residual=None, U=False, out=None, stream=None):
+    """Y [T, R] = act(U) + residual, U = X * Ws^T + bias (float32 [R]); each
+    rounded once to float16.  U=True also returns U (a tensor may be passed
+    instead); returns (Y, U or None).  ``out`` may be the residual."""
+    kind = _act(act)
+    T = X.shape[0]
+    if X.dtype != torch.float16 or tuple(X.shape) != (T, C):
+        raise ValueError("X must be float16 [T, C]")
+    _row_form(vals_row, meta_row, R, C, "the row form")
+    if bias is not None:
+        _need(bias, (R,), torch.float32, "bias")
+    if residual is not None:
+        _need(residual, (T, R), torch.float16, "residual")
+    with _using(stream):
+        out = _out(out, (T, R), torch.float16, X.device)
+        if U is False or U is None:
+            U = None
+        else:
+            U = _out(None if U is True else U, (T, R), torch.float16, X.device)
+    _check("sp24_spmm_fwd_act", lib().sp24_spmm_fwd_act(
+        _ptr(X), _ptr(vals_row), _ptr(meta_row), T, R, C, _ptr(bias), kind, _ptr(residual), _ptr(U), _ptr(out),
+        _stream(stream)))
+    return out, U
+
+
+def sp24_spmm_bwd_input_act(dY, vals_col, meta_col, R, C, U, act="none", dbias=True, out=None, workspace=None,
+                            stream=None):
+    """dU [T, C] = (dY [T, R] * Ws) * act'(U) and dbias [C] (float32), dU's sums
+    over tokens before they are rounded.  dbias=False leaves the sums out (a
+    tensor may be passed instead).  ``out`` may be U, and U None without an
+    activation.  Returns (dU, dbias or None)."""
+    kind = _act(act)
+    T = dY.shape[0]
+    if dY.dtype != torch.float16 or tuple(dY.shape) != (T, R):
+        raise ValueError("dY must be float16 [T, R]")
+    _row_form(vals_col, meta_col, C, R, "the column form")
+    if U is not None or kind:
+        _need(U, (T, C), torch.float16, "U")
+    with _using(stream):
+        out = _out(out, (T, C), torch.float16, dY.device)
+        need = 0
+        if dbias is False or dbias is None:
+            dbias = None
+        else:
+            dbias = _out(None if dbias is True else dbias, (C,), torch.float32, dY.device)
+            need = lib().sp24_spmm_bwd_input_act_workspace(T, R, C)
+        workspace = _workspace(workspace, need, dY.device)
+    _check("sp24_spmm_bwd_input_act", lib().sp24_spmm_bwd_input_act(
+        _ptr(dY), _ptr(vals_col), _ptr(meta_col), T, R, C, kind, _ptr(U), _ptr(out), _ptr(dbias), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, dbias
+
+
+def sp24_bias_grad(dY, dbias=None, workspace=None, stream=None):
+    """dbias [R] (float32): the sums of dY [T, R] (float16) over tokens."""
+    if dY.dtype != torch.float16 or dY.dim() != 2:
+        raise ValueError("dY must be float16 [T, R]")
+    T, R = dY.shape
+    with _using(stream):
+        dbias = _out(dbias, (R,), torch.float32, dY.device)
+        workspace = _workspace(workspace, lib().sp24_bias_grad_workspace(T, R), dY.device)
+    _check("sp24_bias_grad", lib().sp24_bias_grad(_ptr(dY), T, R, _ptr(dbias), _ptr(workspace),
+                                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+    return dbias
+
+
+def step_control(device="cuda"):
+    """What sp24_grad_norm writes and sp24_adamw_step reads (sp24_step_control),
+    before the first step: int32 [8], zeros."""
+    return torch.zeros(8, dtype=torch.int32, device=device)
+
+
+def control_values(control):
+    """Views of a control's fields: step (int64), norm, factor (float32), skip (int32)."""
+    return {"step": control.view(torch.int64)[0], "norm": control.view(torch.float32)[2],
+            "factor": control.view(torch.float32)[3], "skip": control[4]}
+
+
+def _control(control):
+    return _need(control, (8,), torch.int32, "the control")
+
+
+def _pointers(tensors, dtype, name):
+    """Addresses of many tensors; _ptr's checks, each once over all of them."""
+    if any(t.dtype != dtype for t in tensors):
+        raise ValueError(f"{name} must be {dtype}")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous")
+    device = torch.cuda.current_device() if tensors else 0
+    if any([t.get_device() != device for t in tensors]):   # -1 for host memory
+        raise ValueError(f"{name} must be on the current device, cuda:{device}")
+    return [t.data_ptr() for t in tensors]
+
+
+def _grad_type(grads):
+    types = {torch.float16: F16, torch.float32: F32}
+    if grads and grads[0].dtype not in types:
+        raise ValueError("gradients must be float16 or float32")
+    return (grads[0].dtype, types[grads[0].dtype]) if grads else (torch.float32, F32)
+
+
+def sp24_grad_norm(grads, scale=1.0, max_norm=float("inf"), control=None, workspace=None, stream=None):
+    """The norm of all gradients together (all float16 or all float32, of any
+    shapes) times ``scale``, and the factor that takes the scale off them and
+    clips them to ``max_norm``, in a control (see step_control; one is made
+    unless given), whose step grows by 1 unless some gradient is not finite."""
+    dtype, kind = _grad_type(grads)
+    n = len(grads)
+    pointers = (ctypes.c_void_p * n)(*_pointers(grads, dtype, "gradients"))
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    sizes_p = ctypes.cast(sizes, ctypes.c_void_p)
+    with _using(stream):
+        if control is None:
+            control = step_control(torch.device("cuda", torch.cuda.current_device()))
+        _control(control)
+        workspace = _workspace(workspace, lib().sp24_grad_norm_workspace(sizes_p, n), control.device)
+    _check("sp24_grad_norm", lib().sp24_grad_norm(
+        ctypes.cast(pointers, ctypes.c_void_p), sizes_p, n, kind, float(scale), float(max_norm), _ptr(control),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return control
+
+
+class AdamwPlan:
+    """The tensors of an AdamW step, checked once and laid out as the library
+    takes them; sp24_adamw_plan makes one.  It holds the tensors."""
+
+    def __init__(self, jobs, tensors, sizes, state8):
+        self.jobs, self.tensors, self.sizes, self.state8 = jobs, tensors, sizes, state8
+
+
+def sp24_adamw_plan(Ps, Ms, Vs, Ws=None, lrs=1e-3, decays=0.0, M_exps=None, V_exps=None):
+    """The plan of sp24_adamw_step over tensors of any shapes: Ps float32; Ms and
+    Vs float32, or uint8 with M_exps and V_exps (uint8, one for 64 entries: see
+    state8); Ws float16 or None, or None altogether.  lrs and decays are one
+    number for all tensors or one each; decays are the parts of Ps that a step
+    takes off."""
+    n = len(Ps)
+    state8 = M_exps is not None
+    if (V_exps is not None) != state8:
+        raise ValueError("M_exps and V_exps are given together")
+    Ws = [None] * n if Ws is None else Ws
+    lrs, decays = ([float(v)] * n if isinstance(v, (int, float)) else [float(x) for x in v] for v in (lrs, decays))
+    more = (M_exps, V_exps) if state8 else ()
+    if any(len(v) != n for v in (Ms, Vs, Ws, lrs, decays, *more)):
+        raise ValueError("every list needs one entry per tensor")
+    sizes = [P.numel() for P in Ps]
+    dtype = torch.uint8 if state8 else torch.float32
+    for k, (P, M, V, W) in enumerate(zip(Ps, Ms, Vs, Ws)):
+        _need(P, P.shape, torch.float32, "P")
+        _need(M, P.shape, dtype, "M")
+        _need(V, P.shape, dtype, "V")
+        if W is not None:
+            _need(W, P.shape, torch.float16, "W")
+        if state8:
+            _need(M_exps[k], (-(-sizes[k] // 64),), torch.uint8, "M_exps")
+            _need(V_exps[k], (-(-sizes[k] // 64),), torch.uint8, "V_exps")
+    ptr = lambda t: _ptr(t).value if t is not None and t.numel() else None  # noqa: E731
+    jobs = (AdamwJob * n)(*[
+        AdamwJob(None, ptr(Ps[k]), ptr(Ms[k]), ptr(Vs[k]), ptr(M_exps[k]) if state8 else None,
+                 ptr(V_exps[k]) if state8 else None, ptr(Ws[k]), sizes[k], lrs[k], decays[k]) for k in range(n)])
+    return AdamwPlan(jobs, (list(Ps), list(Ms), list(Vs), list(Ws), *more), sizes, state8)
+
+
+def sp24_adamw_step(plan, Gs, betas=(0.9, 0.999), eps=1e-8, step=None, control=None, seed=0, stream=None):
+    """One AdamW step of a plan's tensors, in place, with the gradients ``Gs``
+    (all float16 or all float32): the ``step``-th (1, 2, ...), or as a control
+    that sp24_grad_norm wrote says."""
+    if (step is None) == (control is None):
+        raise ValueError("either step or control")
+    if len(Gs) != len(plan.sizes) or [G.numel() for G in Gs] != plan.sizes:
+        raise ValueError("one gradient per tensor, of its size")
+    dtype, kind = _grad_type(Gs)
+    for job, pointer in zip(plan.jobs, _pointers(Gs, dtype, "gradients")):
+        job.G = pointer
+    if plan.tensors[0] and plan.tensors[0][0].get_device() != torch.cuda.current_device():
+        raise ValueError("the plan's tensors are not on the current device")
+    _check("sp24_adamw_step", lib().sp24_adamw_step(
+        ctypes.cast(plan.jobs, ctypes.c_void_p), len(plan.sizes), kind, STATE8 if plan.state8 else F32, float(betas[0]),
+        float(betas[1]), float(eps), 0 if step is None else int(step),
+        None if control is None else _ptr(_control(control)), int(seed) & 0xFFFFFFFF, _stream(stream)))
+
+
+def state8(P):
+    """An 8-bit state of zeros for a tensor: codes (uint8, P's shape) and
+    exponents (uint8 [ceil(n / 64)])."""
+    return (torch.zeros(P.shape, dtype=torch.uint8, device=P.device),
+            torch.zeros(-(-P.numel() // 64), dtype=torch.uint8, device=P.device))
+
+
+def sp24_state8_values(codes, exps, root=False, dtype=torch.float32, out=None, stream=None):
+    """What an 8-bit state stands for, in codes' shape: M's entries, or with
+    ``root`` the roots of V's; float32 or bfloat16 (which holds them whole)."""
+    types = {torch.float32: F32, torch.bfloat16: BF16}
+    if dtype not in types or codes.dtype != torch.uint8:
+        raise ValueError("codes must be uint8, dtype float32 or bfloat16")
+    _need(exps, (-(-codes.numel() // 64),), torch.uint8, "exps")
+    with _using(stream):
+        out = _out(out, codes.shape, dtype, codes.device)
+    _check("sp24_state8_values", lib().sp24_state8_values(_ptr(codes), _ptr(exps), codes.numel(), int(bool(root)),
+                                                          types[dtype], _ptr(out), _stream(stream)))
+    return out
