@@ -86,7 +86,4 @@ __device__ __forceinline__ void times_slope(int act, const float (&u)[V], float 
   }
 }
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half4 __attribute__((ext_vector_type(4)));
-
 }  // namespace sp24

@@ -33,13 +33,10 @@
 
 #include "sp24_device.hpp"
 #include "sp24_internal.hpp"
+#include "sp24_spmm_tile.hpp"
 
 namespace sp24 {
 namespace {
-
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef _Float16 h16 __attribute__((ext_vector_type(16)));
-typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int BK = 64;            // dense K per stage
 constexpr int A_PAD = 8;          // halves of padding per LDS row
@@ -248,42 +245,6 @@ hipError_t launch_cfg(const uint16_t* A, const uint16_t* vals, const uint16_t* m
   return hipGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// Fast path (K a multiple of 64, every operand below 2 GiB).
-//
-// Workgroup tile BM features x BN tokens in waves of WM x WN (launched as
-// 256 x 256 with 8 waves of 128 x 64, two waves per SIMD).  A 3-stage LDS ring is filled by direct global->LDS buffer
-// loads (no VGPR round trip), two stages ahead of the one being computed, so
-// HBM/L2 latency hides behind two stages of MFMA work.  Rows past N or T read
-// as zero (buffer bounds); they only feed outputs that are not stored.
-//
-// LDS layouts (per stage), both XOR-swizzled so that ds_read_b128 is free of
-// bank conflicts for 8- and 16-lane groups:
-//   S  [BM rows][4 chunks of 16 B]: chunk c of row r at slot c ^ fS(r)
-//   B  [BN rows][8 chunks of 16 B]: chunk c of row r at slot c ^ fB(r)
-//   meta [BM rows][2 dwords]
-// A direct load writes 64 consecutive 16-byte LDS slots, one per lane, so each
-// lane fetches the global chunk whose swizzled slot is its own lane index.
-
-__device__ __forceinline__ int swz_s(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
-__device__ __forceinline__ int swz_b(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
-template <int BM, int BN, int WM, int WN>
-struct FastCfg {
-  static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN;
-  static constexpr int WAVES = WAVES_M * WAVES_N;
-  static constexpr int THREADS = 64 * WAVES;
-  static constexpr int TM = WM / 32, TN = WN / 32;
-  static constexpr int S_BYTES = BM * 64, B_BYTES = BN * 128, M_BYTES = BM * 8;
-  static constexpr int S_LOADS = S_BYTES / 1024 / WAVES;   // 16-byte direct loads per wave per stage
-  static constexpr int B_LOADS = B_BYTES / 1024 / WAVES;
-  static constexpr int M_LOADS = M_BYTES / 256 / WAVES;    // 4-byte direct loads
-  static constexpr int LOADS = S_LOADS + B_LOADS + M_LOADS;
-  static_assert(S_BYTES % (1024 * WAVES) == 0 && B_BYTES % (1024 * WAVES) == 0 && M_BYTES % (256 * WAVES) == 0,
-                "tile does not split evenly into direct loads");
-  static_assert(LOADS <= 63, "vmcnt range");
-};
-
 // One BM x BN output tile at tile coordinates (tm, tn), computed by the
 // whole workgroup with the ring in `smem`.  When `post` is set, thread 0
 // stores `post_val` to *post_dst once the K loop is done, before the
@@ -295,214 +256,7 @@ __device__ __forceinline__ void spmm_fast_tile(unsigned char* __restrict__ smem,
                                                int64_t T, int64_t N, int64_t K, uint16_t* __restrict__ out,
                                                int64_t ldo, uint16_t* __restrict__ gout, int64_t ldg, int tm, int tn,
                                                int tid, bool post, int* post_dst, int post_val) {
-  using Cfg = FastCfg<BM, BN, WM, WN>;
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-
-  // the wave index is uniform across the wave; say so, since the direct
-  // loads take their LDS destination from a scalar register
-  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % Cfg::WAVES_M, wn = wave / Cfg::WAVES_M;
-  const int l32 = lane & 31, g = lane >> 5;
-  const int nk = (int)(K / 64);
-
-  // buffer resources based at this tile's first row; bytes past the matrix
-  // end are out of range and load as zero.  S and meta are in blocked order:
-  // a band of 64 rows starts every band_s (band_m) bytes, and stage kt of a
-  // band of h rows is its contiguous block at kt * h * 64 (kt * h * 8) bytes.
-  // Each load's rows (16 of S, 32 of meta) lie in one band, so its stage
-  // stride st_s (st_m) is uniform across the wave: 4096 (512) for a full
-  // band.  In the last band of an N % 64 != 0 operand, rows past N read bytes
-  // of other rows or of nothing (zero); both only feed outputs that are not
-  // stored.  Bands wholly past N start beyond the range.
-  const i32x4 rs = make_rsrc(vals + m0 * (K / 2), (uint32_t)((N - m0) * K));
-  const i32x4 rb = make_rsrc(A + n0 * K, (uint32_t)((T - n0) * K * 2));
-  const i32x4 rm = make_rsrc(meta + m0 * (K / 16), (uint32_t)((N - m0) * (K / 8)));
-  const int band_s = 64 * (int)K, band_m = 8 * (int)K;
-  auto band_rows = [&](int band) {
-    const int64_t left = N - m0 - 64 * band;
-    return (int)(left >= 64 ? 64 : left > 0 ? left : 0);
-  };
-  int st_s[Cfg::S_LOADS], st_m[Cfg::M_LOADS];
-#pragma unroll
-  for (int i = 0; i < Cfg::S_LOADS; ++i) st_s[i] = band_rows((wave * Cfg::S_LOADS + i) / 4) * 64;
-#pragma unroll
-  for (int i = 0; i < Cfg::M_LOADS; ++i) st_m[i] = band_rows((wave * Cfg::M_LOADS + i) / 2) * 8;
-
-  // per-lane global byte offsets of this wave's direct loads (stage 0)
-  int off_s[Cfg::S_LOADS], off_b[Cfg::B_LOADS], off_m[Cfg::M_LOADS];
-#pragma unroll
-  for (int i = 0; i < Cfg::S_LOADS; ++i) {
-    const int q = wave * Cfg::S_LOADS + i;          // 1 KiB: rows 16q .. 16q+15, contiguous in their block
-    const int r = 16 * q + lane / 4, p = lane % 4;
-    off_s[i] = (r / 64) * band_s + (r % 64) * 64 + ((p ^ swz_s(r)) * 16);
-  }
-#pragma unroll
-  for (int i = 0; i < Cfg::B_LOADS; ++i) {
-    const int q = wave * Cfg::B_LOADS + i;          // rows 8q .. 8q+7
-    const int r = 8 * q + lane / 8, p = lane % 8;
-    off_b[i] = r * K * 2 + ((p ^ swz_b(r)) * 16);
-  }
-#pragma unroll
-  for (int i = 0; i < Cfg::M_LOADS; ++i) {
-    const int q = wave * Cfg::M_LOADS + i;          // rows 32q .. 32q+31
-    const int r = 32 * q + lane / 2;
-    off_m[i] = (r / 64) * band_m + (r % 64) * 8 + (lane % 2) * 4;
-  }
-
-  // one of this wave's LOADS direct loads of stage kt (j in [0, LOADS))
-  auto issue_one = [&](int j, int kt, unsigned char* sb, unsigned char* bb, unsigned char* mb) {
-    if (j < Cfg::S_LOADS) {
-      dma_b128(rs, lds_addr(sb) + (wave * Cfg::S_LOADS + j) * 1024, off_s[j] + kt * st_s[j]);
-    } else if (j < Cfg::S_LOADS + Cfg::B_LOADS) {
-      const int i = j - Cfg::S_LOADS;
-      dma_b128(rb, lds_addr(bb) + (wave * Cfg::B_LOADS + i) * 1024, off_b[i] + kt * 128);
-    } else {
-      const int i = j - Cfg::S_LOADS - Cfg::B_LOADS;
-      dma_b32(rm, lds_addr(mb) + (wave * Cfg::M_LOADS + i) * 256, off_m[i] + kt * st_m[i]);
-    }
-  };
-  auto issue = [&](int kt, unsigned char* sb, unsigned char* bb, unsigned char* mb) {
-    const int db = kt * 128;
-#pragma unroll
-    for (int i = 0; i < Cfg::S_LOADS; ++i)
-      dma_b128(rs, lds_addr(sb) + (wave * Cfg::S_LOADS + i) * 1024, off_s[i] + kt * st_s[i]);
-#pragma unroll
-    for (int i = 0; i < Cfg::B_LOADS; ++i)
-      dma_b128(rb, lds_addr(bb) + (wave * Cfg::B_LOADS + i) * 1024, off_b[i] + db);
-#pragma unroll
-    for (int i = 0; i < Cfg::M_LOADS; ++i)
-      dma_b32(rm, lds_addr(mb) + (wave * Cfg::M_LOADS + i) * 256, off_m[i] + kt * st_m[i]);
-  };
-
-  // LDS read offsets of this lane (bytes), independent of the stage
-  const int fs = swz_s(l32), fb = swz_b(l32);
-  int rd_s[2];
-#pragma unroll
-  for (int st = 0; st < 2; ++st) rd_s[st] = (wm * WM + l32) * 64 + (((2 * st + g) ^ fs) * 16);
-  int rd_b[2][2];
-#pragma unroll
-  for (int st = 0; st < 2; ++st)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) rd_b[st][h] = (wn * WN + l32) * 128 + (((4 * st + 2 * h + g) ^ fb) * 16);
-  const int rd_m = (wm * WM + l32) * 8;
-
-  f16v acc[Cfg::TM][Cfg::TN];
-#pragma unroll
-  for (int i = 0; i < Cfg::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < Cfg::TN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-
-  // register fragments of one K32 step
-  struct Frags {
-    h8 a[Cfg::TM];
-    h16 b[Cfg::TN];
-  };
-  auto load_frags = [&](const unsigned char* sb, const unsigned char* bb, int st, Frags& f) {
-#pragma unroll
-    for (int mt = 0; mt < Cfg::TM; ++mt) f.a[mt] = *reinterpret_cast<const h8*>(sb + rd_s[st] + mt * 32 * 64);
-#pragma unroll
-    for (int nt = 0; nt < Cfg::TN; ++nt) {
-      const h8 lo = *reinterpret_cast<const h8*>(bb + rd_b[st][0] + nt * 32 * 128);
-      const h8 hi = *reinterpret_cast<const h8*>(bb + rd_b[st][1] + nt * 32 * 128);
-      f.b[nt] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
-    }
-  };
-  // meta words of this lane's rows for both K32 steps of a stage
-  auto load_meta = [&](const unsigned char* mb, uint2 (&mw)[Cfg::TM]) {
-#pragma unroll
-    for (int mt = 0; mt < Cfg::TM; ++mt) mw[mt] = *reinterpret_cast<const uint2*>(mb + rd_m + mt * 32 * 8);
-  };
-  // The SMFMACs of one K32 step.  Two waves share each SIMD; raising the
-  // priority of the wave in its MFMA block lets it issue back to back while
-  // the other wave issues its LDS reads and direct loads in between.  When
-  // kt_load >= 0, this wave's direct loads of stage kt_load go out one after
-  // each SMFMAC rather than in a burst, so the texture unit drains steadily
-  // and no wave stalls long on its in-order vector-memory issue.
-  auto mfmas = [&](const Frags& f, const uint2 (&mw)[Cfg::TM], int st, int kt_load, unsigned char* sb,
-                   unsigned char* bb, unsigned char* mb) {
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int mt = 0; mt < Cfg::TM; ++mt) {
-      const uint32_t w = st ? mw[mt].y : mw[mt].x;
-      const int idx = (int)(g ? (w >> 16) : w);
-#pragma unroll
-      for (int nt = 0; nt < Cfg::TN; ++nt) {
-        acc[mt][nt] = __builtin_amdgcn_smfmac_f32_32x32x32_f16(f.a[mt], f.b[nt], acc[mt][nt], idx, 0, 0);
-        const int j = mt * Cfg::TN + nt;
-        if (j < Cfg::LOADS && kt_load >= 0) issue_one(j, kt_load, sb, bb, mb);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-#pragma unroll
-    for (int j = Cfg::TM * Cfg::TN; j < Cfg::LOADS; ++j)
-      if (kt_load >= 0) issue_one(j, kt_load, sb, bb, mb);
-    __builtin_amdgcn_s_setprio(0);
-  };
-
-  // vmcnt wait: allow `stages` stages of this wave's direct loads in flight
-  auto wait_loads = [&](int stages) {
-    // vmcnt in bits 3:0 and 15:14; expcnt 7 and lgkmcnt 15 mean no wait
-    if (stages >= 2) {
-      constexpr int n = 2 * Cfg::LOADS;
-      __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-    } else if (stages == 1) {
-      constexpr int n = Cfg::LOADS;
-      __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-    } else {
-      __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
-    }
-  };
-
-  unsigned char* const s_buf[3] = {smem, smem + Cfg::S_BYTES, smem + 2 * Cfg::S_BYTES};
-  unsigned char* const b_buf[3] = {smem + 3 * Cfg::S_BYTES, smem + 3 * Cfg::S_BYTES + Cfg::B_BYTES,
-                                   smem + 3 * Cfg::S_BYTES + 2 * Cfg::B_BYTES};
-  unsigned char* const m_buf[3] = {smem + 3 * (Cfg::S_BYTES + Cfg::B_BYTES),
-                                   smem + 3 * (Cfg::S_BYTES + Cfg::B_BYTES) + Cfg::M_BYTES,
-                                   smem + 3 * (Cfg::S_BYTES + Cfg::B_BYTES) + 2 * Cfg::M_BYTES};
-
-  // Pipeline.  Stage s (64 of K) is loaded into ring slot s % 3 three stages
-  // ahead.  Within stage kt: the fragments of its second K32 step are read
-  // while the first step's MFMAs run; then, mid-stage, the wave waits for
-  // stage kt+1 to land, all waves meet at a barrier (after which nobody reads
-  // slot kt % 3 again), stage kt+3 is issued into that slot, and the first
-  // fragments of stage kt+1 are read while the second step's MFMAs run.
-  for (int s = 0; s < 3; ++s)
-    if (s < nk) issue(s, s_buf[s], b_buf[s], m_buf[s]);
-  wait_loads(min(nk, 3) - 1);
-  __builtin_amdgcn_s_barrier();
-  Frags f0, f1;
-  uint2 mw[Cfg::TM], mw_next[Cfg::TM];
-  load_meta(m_buf[0], mw);
-  load_frags(s_buf[0], b_buf[0], 0, f0);
-
-  auto stage = [&](int kt, int cur, int nxt) {
-    load_frags(s_buf[cur], b_buf[cur], 1, f1);
-    __builtin_amdgcn_sched_barrier(0);
-    mfmas(f0, mw, 0, -1, nullptr, nullptr, nullptr);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_loads(kt + 2 < nk ? 1 : 0);
-    // lgkmcnt(0): this wave's reads of slot kt % 3 are complete before the
-    // barrier lets stage kt+3 overwrite it (vmcnt 63, expcnt 7 = no wait)
-    __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));
-    __builtin_amdgcn_s_barrier();
-    if (kt + 1 < nk) {
-      load_meta(m_buf[nxt], mw_next);
-      load_frags(s_buf[nxt], b_buf[nxt], 0, f0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    // stage kt+3 goes into slot kt % 3, free since the barrier
-    mfmas(f1, mw, 1, kt + 3 < nk ? kt + 3 : -1, s_buf[cur], b_buf[cur], m_buf[cur]);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int mt = 0; mt < Cfg::TM; ++mt) mw[mt] = mw_next[mt];
-  };
-  for (int kt = 0; kt < nk; kt += 3) {
-    stage(kt, 0, 1);
-    if (kt + 1 < nk) stage(kt + 1, 1, 2);
-    if (kt + 2 < nk) stage(kt + 2, 2, 0);
-  }
+#include "sp24_spmm_loop.inc"
 
   // Epilogue: fp32 -> fp16 (round to nearest even).  Each wave stages its
   // WN tokens x WM features in LDS (token-major, 16-byte chunks XOR-swizzled
