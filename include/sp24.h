@@ -607,8 +607,8 @@ enum {
  *   residual  in   fp16 [T, R], or NULL
  *   U         out  fp16 [T, R], or NULL
  *   Y         out  fp16 [T, R]; may be the residual's own memory
- * Infinite U gives what the formulas give in IEEE arithmetic (NaN for -inf with
- * GELU, GELU_TANH and SILU); NaN gives NaN.
+ * U of +inf gives +inf; of -inf 0 with RELU, RELU2 and GELU, NaN with GELU_TANH
+ * and SILU (-inf * 0); NaN gives NaN.
  * Errors: NULL, SHAPE, ALIGN, LAUNCH; UNSUPPORTED for another act; TOO_LARGE as
  * for sp24_spmm_fwd, and when R reaches 2^27.
  */

@@ -8,15 +8,42 @@
 
 namespace sp24 {
 
-// 1 / (1 + exp(-z)) through the hardware's 2^y and reciprocal, each within
-// 1 ulp: about 2e-7 relative, and z's own rounding.  exp(-z) may overflow to
-// infinity: the reciprocal is 0 then.
-__device__ __forceinline__ float logistic(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+// 1 / (1 + 2^z) with the hardware's 2^z and reciprocal, within 1 ulp each; z's
+// rounding adds |z| 2^-23.  2^z may overflow to infinity: the reciprocal is 0
+// then.
+__device__ __forceinline__ float logistic2(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z));
 }
 
-// GELU's tanh form, x/2 (1 + tanh(k/2 (x + c x^3))) = x / (1 + exp(-k (x + c x^3)))
-constexpr float kTanhK = 1.5957691216f /* 2 sqrt(2 / pi) */, kTanhC = 0.044715f;
+constexpr float kLog2 = 1.44269504f, kLog2InvSqrt2Pi = -1.32574806f;   // log2 e, log2(1 / sqrt(2 pi))
+// x/2 (1 + tanh(sqrt(2 / pi) (x + c x^3))) = x / (1 + exp(-k (x + c x^3))), k = 2 sqrt(2 / pi)
+constexpr float kTanhC = 0.044715f, kTanhK = 1.5957691216f;
+
+// GELU: Phi(-a) = 2^P(a) for a = |x|, with the P of degree 6 that
+// gen_gelu_fit.py prints: within 1.4e-6 relative, or a Phi(-a) within 4e-9, and
+// |P| 2^-23 by rounding (1e-6 at a = 4), thousandths of fp16's half step.  One
+// exponential and no division: about 16 issue slots for x Phi(x), counting 4 for
+// the exponential, where sp24_device.hpp's form, which keeps 7e-7 relative as
+// far as fp32 goes, takes 36 (forward product of 16384 x 6400 x 1600: 312 us
+// with that, 290 with this).  P falls up to a = 13; past 10 it is held there,
+// with x Phi(x) below 1e-22.
+constexpr float kTail[7] = {-9.9999785e-01f, -1.1511753e+00f, -4.587958e-01f, -5.3436358e-02f,
+                            8.12274e-03f,    -7.875215e-04f,  3.5610567e-05f};
+__device__ __forceinline__ float normal_tail(float a) {
+  float p = kTail[6];
+#pragma unroll
+  for (int k = 5; k >= 0; --k) p = __builtin_fmaf(p, a, kTail[k]);
+  return __builtin_amdgcn_exp2f(p);
+}
+// min(|x|, 10), NaN for NaN
+__device__ __forceinline__ float tail_argument(float x) {
+  const float a = __builtin_fabsf(x);
+  return a > 10.0f ? 10.0f : a;
+}
+
+__device__ __forceinline__ float tanh_form(float x, float x2) {
+  return logistic2(x * __builtin_fmaf(x2, -kLog2 * kTanhK * kTanhC, -kLog2 * kTanhK));
+}
 
 // act(u) of V values.  The kind is the same in all lanes, so a wave takes one
 // branch for its V values.
@@ -33,15 +60,19 @@ __device__ __forceinline__ void activate(int act, float (&u)[V]) {
       break;
     case kActGelu:
 #pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = gelu_f32(u[e]);
+      for (int e = 0; e < V; ++e) {
+        // x Phi(x) = max(x, 0) - a Phi(-a)
+        const float a = tail_argument(u[e]);
+        u[e] = __builtin_fmaf(-a, normal_tail(a), u[e] < 0.0f ? 0.0f : u[e]);
+      }
       break;
     case kActGeluTanh:
 #pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = u[e] * logistic(kTanhK * u[e] * __builtin_fmaf(kTanhC * u[e], u[e], 1.0f));
+      for (int e = 0; e < V; ++e) u[e] = u[e] * tanh_form(u[e], u[e] * u[e]);
       break;
     case kActSilu:
 #pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = u[e] * logistic(u[e]);
+      for (int e = 0; e < V; ++e) u[e] = u[e] * logistic2(u[e] * -kLog2);
       break;
     default: break;
   }
@@ -62,23 +93,25 @@ __device__ __forceinline__ void times_slope(int act, const float (&u)[V], float 
     case kActGelu:
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        float cdf, pdf;
-        gelu_cdf_pdf(u[e], cdf, pdf);
-        d[e] *= __builtin_fmaf(u[e], pdf, cdf);
+        // Phi(x) + x phi(x): Phi(-a) - a phi(a) on the left, 1 less that on the right
+        const float a = tail_argument(u[e]);
+        const float pdf = __builtin_amdgcn_exp2f(__builtin_fmaf(a * a, -0.5f * kLog2, kLog2InvSqrt2Pi));
+        const float left = __builtin_fmaf(-a, pdf, normal_tail(a));
+        d[e] *= u[e] < 0.0f ? left : 1.0f - left;
       }
       break;
     case kActGeluTanh:
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float x2 = u[e] * u[e];
-        const float s = logistic(kTanhK * u[e] * __builtin_fmaf(kTanhC, x2, 1.0f));
+        const float s = tanh_form(u[e], x2);
         d[e] *= __builtin_fmaf(u[e] * s * (1.0f - s), kTanhK * __builtin_fmaf(3.0f * kTanhC, x2, 1.0f), s);
       }
       break;
     case kActSilu:
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float s = logistic(u[e]);
+        const float s = logistic2(u[e] * -kLog2);
         d[e] *= __builtin_fmaf(u[e] * s, 1.0f - s, s);
       }
       break;

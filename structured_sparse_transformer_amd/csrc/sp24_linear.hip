@@ -253,6 +253,19 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
   if (!kBwd && fin.bias != nullptr && inside)
 #pragma unroll
     for (int e = 0; e < 8; ++e) bias[e] = fin.bias[m + e];
+  // What the epilogue reads beside the sums (the residual, or U) is fetched
+  // kAhead passes of 4 tokens early, rows past the last one from the last one.
+  const uint16_t* const beside = kBwd ? fin.u_in : fin.add;
+  constexpr int kAhead = 4;
+  h8 next[kAhead];
+  const int first = lane >> 4, last = (int)T - 1;
+  const uint16_t* const from_m = beside + t0 * ld + (inside ? m : 0);
+  const auto fetch = [&](int pass) {
+    return *reinterpret_cast<const h8*>(from_m + (int64_t)min(wn * WN + pass * 4 + first, last) * ld);
+  };
+  if (beside != nullptr)
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) next[k] = fetch(k);
   float sums[8] = {};
 #pragma unroll
   for (int nt = 0; nt < Cfg::TN; ++nt) {
@@ -265,22 +278,28 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
             float4v{a[4 * i4], a[4 * i4 + 1], a[4 * i4 + 2], a[4 * i4 + 3]};
       }
     // the wave reads back only what it wrote, in order: no barrier is needed
+#pragma unroll 2
     for (int it = 0; it < 8; ++it) {
-      const int t = it * 4 + (lane >> 4);
+      const int t = it * 4 + first;
       const unsigned char* const from = staged + t * 512 + ((q ^ (t & 15)) * 16);
       const float4v lo = *reinterpret_cast<const float4v*>(from);
       const float4v hi = *reinterpret_cast<const float4v*>(from + 256);
-      const int64_t n = wn * WN + nt * 32 + t;
-      if (n >= T || !inside) continue;
+      const h8 now = next[0];
+      if (beside != nullptr) {
+#pragma unroll
+        for (int k = 1; k < kAhead; ++k) next[k - 1] = next[k];
+        next[kAhead - 1] = fetch(nt * 8 + it + kAhead);
+      }
+      const int n = wn * WN + nt * 32 + t;
+      if (n > last || !inside) continue;
       const int64_t at = (t0 + n) * ld + m;
       float d[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       if constexpr (kBwd) {
-        if (fin.u_in != nullptr) {
-          const h8 u = *reinterpret_cast<const h8*>(fin.u_in + at);
-          float uf[8];
+        if (beside != nullptr) {
+          float u[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) uf[e] = (float)u[e];
-          times_slope(fin.act, uf, d);
+          for (int e = 0; e < 8; ++e) u[e] = (float)now[e];
+          times_slope(fin.act, u, d);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[e] += d[e];
@@ -294,11 +313,9 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
           *reinterpret_cast<h8*>(fin.u_out + at) = u;
         }
         activate(fin.act, d);
-        if (fin.add != nullptr) {
-          const h8 r = *reinterpret_cast<const h8*>(fin.add + at);
+        if (beside != nullptr)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] += (float)r[e];
-        }
+          for (int e = 0; e < 8; ++e) d[e] += (float)now[e];
       }
       h8 y;
 #pragma unroll
@@ -414,21 +431,35 @@ hipError_t launch_product(const uint16_t* A, const uint16_t* vals, const uint16_
 // ---------------------------------------------------------------------------
 // Sums over rows.
 
-// out[c] = the sum of part[P][N]'s rows, in order: P rows for columns below
-// `split`, Q for the others.
-__global__ __launch_bounds__(256) void join_rows_kernel(const float* __restrict__ part, int64_t P, int64_t split,
+// out[c] = the sum of part[P][N]'s rows: P rows for columns below `split` (a
+// multiple of 64), Q for the others.  Eight waves take every eighth row, eight
+// rows at a time, of 64 columns, and their sums are added in order.
+__global__ __launch_bounds__(512) void join_rows_kernel(const float* __restrict__ part, int64_t P, int64_t split,
                                                         int64_t Q, int64_t N, float* __restrict__ out) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
-  if (c >= split) P = Q;
+  __shared__ float waves[8][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  if (c - lane >= split) P = Q;
   float v = 0.0f;
-  for (int64_t p = 0; p < P; ++p) v += part[p * N + c];
+  if (c < N)
+    for (int64_t p = wave; p < P; p += 64) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = p + 8 * k < P ? part[(p + 8 * k) * N + c] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += x[k];
+    }
+  waves[wave][lane] = v;
+  __syncthreads();
+  if (wave != 0 || c >= N) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) v += waves[w][lane];
   out[c] = v;
 }
 
 hipError_t launch_join_rows(const float* part, int64_t P, int64_t split, int64_t Q, int64_t N, float* out,
                             hipStream_t s) {
-  hipLaunchKernelGGL(join_rows_kernel, dim3((unsigned)((N + 255) / 256)), dim3(256), 0, s, part, P, split, Q, N, out);
+  hipLaunchKernelGGL(join_rows_kernel, dim3((unsigned)((N + 63) / 64)), dim3(512), 0, s, part, P, split, Q, N, out);
   return hipGetLastError();
 }
 
@@ -442,10 +473,14 @@ __global__ __launch_bounds__(256) void column_sums_kernel(const uint16_t* __rest
   const int64_t first = (int64_t)blockIdx.y * rows, last = min<int64_t>(T, first + rows);
   float v[8] = {};
   if (c < R)
-    for (int64_t t = first + wave; t < last; t += 4) {
-      const h8 x = *reinterpret_cast<const h8*>(dY + t * R + c);
+    for (int64_t t = first + wave; t < last; t += 32) {
+      h8 x[8];   // eight rows under way at once
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += (float)x[e];
+      for (int k = 0; k < 8; ++k) x[k] = t + 4 * k < last ? *reinterpret_cast<const h8*>(dY + (t + 4 * k) * R + c) : h8{};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += (float)x[k][e];
     }
 #pragma unroll
   for (int e = 0; e < 8; ++e) part[wave][lane * 8 + e] = v[e];

@@ -480,9 +480,12 @@ def _id_type(ids):
     return types[ids.dtype]
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _using(stream):
     """What is allocated within belongs to the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE_AND_NOW if stream is None else torch.cuda.stream(stream)
 
 
 def _workspace(t, need, device):
@@ -639,28 +642,40 @@ def _act(name):
     return ACTIVATIONS[name]
 
 
+def _addresses(*tensors):
+    """_ptr of a call's tensors, as plain numbers (0: NULL): a call of one token
+    costs as much in here as on the GPU."""
+    device, res = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0, []
+    for t in tensors:
+        if t is None:
+            res.append(None)
+            continue
+        if t.get_device() != device:   # -1 for host memory
+            _ptr(t)
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        res.append(t.data_ptr() or None)
+    return res
+
+
 def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residual=None, U=False, out=None, stream=None):
     """Y [T, R] = act(U) + residual, U = X * Ws^T + bias (float32 [R]); each
     rounded once to float16.  U=True also returns U (a tensor may be passed
     instead); returns (Y, U or None).  ``out`` may be the residual."""
-    kind = _act(act)
+    kind, f16 = _act(act), torch.float16
     T = X.shape[0]
-    if X.dtype != torch.float16 or tuple(X.shape) != (T, C):
+    if X.dtype != f16 or X.shape != (T, C):
         raise ValueError("X must be float16 [T, C]")
     _row_form(vals_row, meta_row, R, C, "the row form")
-    if bias is not None:
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (R,)):
         _need(bias, (R,), torch.float32, "bias")
-    if residual is not None:
-        _need(residual, (T, R), torch.float16, "residual")
+    if residual is not None and (residual.dtype != f16 or residual.shape != (T, R)):
+        _need(residual, (T, R), f16, "residual")
     with _using(stream):
-        out = _out(out, (T, R), torch.float16, X.device)
-        if U is False or U is None:
-            U = None
-        else:
-            U = _out(None if U is True else U, (T, R), torch.float16, X.device)
-    _check("sp24_spmm_fwd_act", lib().sp24_spmm_fwd_act(
-        _ptr(X), _ptr(vals_row), _ptr(meta_row), T, R, C, _ptr(bias), kind, _ptr(residual), _ptr(U), _ptr(out),
-        _stream(stream)))
+        out = _out(out, (T, R), f16, X.device)
+        U = None if U is False or U is None else _out(None if U is True else U, (T, R), f16, X.device)
+    x, v, m, b, r, u, y = _addresses(X, vals_row, meta_row, bias, residual, U, out)
+    _check("sp24_spmm_fwd_act", lib().sp24_spmm_fwd_act(x, v, m, T, R, C, b, kind, r, u, y, _stream(stream)))
     return out, U
 
 
@@ -670,25 +685,26 @@ def sp24_spmm_bwd_input_act(dY, vals_col, meta_col, R, C, U, act="none", dbias=T
     over tokens before they are rounded.  dbias=False leaves the sums out (a
     tensor may be passed instead).  ``out`` may be U, and U None without an
     activation.  Returns (dU, dbias or None)."""
-    kind = _act(act)
+    kind, f16 = _act(act), torch.float16
     T = dY.shape[0]
-    if dY.dtype != torch.float16 or tuple(dY.shape) != (T, R):
+    if dY.dtype != f16 or dY.shape != (T, R):
         raise ValueError("dY must be float16 [T, R]")
     _row_form(vals_col, meta_col, C, R, "the column form")
     if U is not None or kind:
-        _need(U, (T, C), torch.float16, "U")
+        _need(U, (T, C), f16, "U")
+    L, need = lib(), 0
     with _using(stream):
-        out = _out(out, (T, C), torch.float16, dY.device)
-        need = 0
+        out = _out(out, (T, C), f16, dY.device)
         if dbias is False or dbias is None:
             dbias = None
         else:
             dbias = _out(None if dbias is True else dbias, (C,), torch.float32, dY.device)
-            need = lib().sp24_spmm_bwd_input_act_workspace(T, R, C)
-        workspace = _workspace(workspace, need, dY.device)
-    _check("sp24_spmm_bwd_input_act", lib().sp24_spmm_bwd_input_act(
-        _ptr(dY), _ptr(vals_col), _ptr(meta_col), T, R, C, kind, _ptr(U), _ptr(out), _ptr(dbias), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+            need = L.sp24_spmm_bwd_input_act_workspace(T, R, C)
+        workspace = _workspace(workspace, need, dY.device) if need else None
+    y, v, m, u, o, b, w = _addresses(dY, vals_col, meta_col, U, out, dbias, workspace)
+    _check("sp24_spmm_bwd_input_act", L.sp24_spmm_bwd_input_act(
+        y, v, m, T, R, C, kind, u, o, b, w, 0 if w is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
     return out, dbias
 
 
@@ -697,11 +713,14 @@ def sp24_bias_grad(dY, dbias=None, workspace=None, stream=None):
     if dY.dtype != torch.float16 or dY.dim() != 2:
         raise ValueError("dY must be float16 [T, R]")
     T, R = dY.shape
+    L = lib()
+    need = L.sp24_bias_grad_workspace(T, R)
     with _using(stream):
         dbias = _out(dbias, (R,), torch.float32, dY.device)
-        workspace = _workspace(workspace, lib().sp24_bias_grad_workspace(T, R), dY.device)
-    _check("sp24_bias_grad", lib().sp24_bias_grad(_ptr(dY), T, R, _ptr(dbias), _ptr(workspace),
-                                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace = _workspace(workspace, need, dY.device) if need else None
+    y, b, w = _addresses(dY, dbias, workspace)
+    _check("sp24_bias_grad", L.sp24_bias_grad(
+        y, T, R, b, w, 0 if w is None else workspace.numel() * workspace.element_size(), _stream(stream)))
     return dbias
 
 

@@ -219,7 +219,7 @@ def test_infinite_and_nan(sp):
     bias = torch.zeros(64, device="cuda")
     bias[:3] = torch.tensor([float("inf"), float("-inf"), float("nan")])
     zero = torch.zeros(2, 64, dtype=torch.float16, device="cuda")
-    for act, low in zip(ACTS, (-math.inf, 0.0, 0.0, math.nan, math.nan, math.nan)):
+    for act, low in zip(ACTS, (-math.inf, 0.0, 0.0, 0.0, math.nan, math.nan)):
         Y, _ = sp.sp24_spmm_fwd_act(zero, f["vals_row"], f["meta_row"], 64, 64, act=act, bias=bias)
         got = Y[0, :3].tolist()
         assert got[0] == math.inf and math.isnan(got[2])
