@@ -2,6 +2,7 @@
 #pragma once
 #include <hip/hip_runtime.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "sp24_device.hpp"
 #include "sp24_internal.hpp"
@@ -45,77 +46,55 @@ __device__ __forceinline__ float tanh_form(float x, float x2) {
   return logistic2(x * __builtin_fmaf(x2, -kLog2 * kTanhK * kTanhC, -kLog2 * kTanhK));
 }
 
-// act(u) of V values.  The kind is the same in all lanes, so a wave takes one
-// branch for its V values.
-template <int V>
-__device__ __forceinline__ void activate(int act, float (&u)[V]) {
-  switch (act) {
-    case kActRelu:
-#pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = u[e] < 0.0f ? 0.0f : u[e];
-      break;
-    case kActRelu2:
-#pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = u[e] < 0.0f ? 0.0f : u[e] * u[e];
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        // x Phi(x) = max(x, 0) - a Phi(-a)
-        const float a = tail_argument(u[e]);
-        u[e] = __builtin_fmaf(-a, normal_tail(a), u[e] < 0.0f ? 0.0f : u[e]);
-      }
-      break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = u[e] * tanh_form(u[e], u[e] * u[e]);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int e = 0; e < V; ++e) u[e] = u[e] * logistic2(u[e] * -kLog2);
-      break;
-    default: break;
+// act(u)
+template <int kAct>
+__device__ __forceinline__ float activate(float u) {
+  if constexpr (kAct == kActRelu) return u < 0.0f ? 0.0f : u;
+  if constexpr (kAct == kActRelu2) return u < 0.0f ? 0.0f : u * u;
+  if constexpr (kAct == kActGelu) {
+    // x Phi(x) = max(x, 0) - a Phi(-a)
+    const float a = tail_argument(u);
+    return __builtin_fmaf(-a, normal_tail(a), u < 0.0f ? 0.0f : u);
   }
+  if constexpr (kAct == kActGeluTanh) return u * tanh_form(u, u * u);
+  if constexpr (kAct == kActSilu) return u * logistic2(u * -kLog2);
+  return u;
 }
 
-// d[e] *= act'(u[e]).
-template <int V>
-__device__ __forceinline__ void times_slope(int act, const float (&u)[V], float (&d)[V]) {
+// d act'(u)
+template <int kAct>
+__device__ __forceinline__ float times_slope(float d, float u) {
+  if constexpr (kAct == kActRelu) return u > 0.0f ? d : 0.0f;
+  if constexpr (kAct == kActRelu2) return u > 0.0f ? d * (2.0f * u) : 0.0f;
+  if constexpr (kAct == kActGelu) {
+    // Phi(x) + x phi(x): Phi(-a) - a phi(a) on the left, 1 less that on the right
+    const float a = tail_argument(u);
+    const float pdf = __builtin_amdgcn_exp2f(__builtin_fmaf(a * a, -0.5f * kLog2, kLog2InvSqrt2Pi));
+    const float left = __builtin_fmaf(-a, pdf, normal_tail(a));
+    return d * (u < 0.0f ? left : 1.0f - left);
+  }
+  if constexpr (kAct == kActGeluTanh) {
+    const float x2 = u * u, s = tanh_form(u, x2);
+    return d * __builtin_fmaf(u * s * (1.0f - s), kTanhK * __builtin_fmaf(3.0f * kTanhC, x2, 1.0f), s);
+  }
+  if constexpr (kAct == kActSilu) {
+    const float s = logistic2(u * -kLog2);
+    return d * __builtin_fmaf(u * s, 1.0f - s, s);
+  }
+  return d;
+}
+
+// f(kind) with the activation as a constant.  It is the same in all lanes: a
+// wave takes one branch.
+template <class F>
+__device__ __forceinline__ void with_act(int act, const F& f) {
   switch (act) {
-    case kActRelu:
-#pragma unroll
-      for (int e = 0; e < V; ++e) d[e] = u[e] > 0.0f ? d[e] : 0.0f;
-      break;
-    case kActRelu2:
-#pragma unroll
-      for (int e = 0; e < V; ++e) d[e] = u[e] > 0.0f ? d[e] * (2.0f * u[e]) : 0.0f;
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        // Phi(x) + x phi(x): Phi(-a) - a phi(a) on the left, 1 less that on the right
-        const float a = tail_argument(u[e]);
-        const float pdf = __builtin_amdgcn_exp2f(__builtin_fmaf(a * a, -0.5f * kLog2, kLog2InvSqrt2Pi));
-        const float left = __builtin_fmaf(-a, pdf, normal_tail(a));
-        d[e] *= u[e] < 0.0f ? left : 1.0f - left;
-      }
-      break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float x2 = u[e] * u[e];
-        const float s = tanh_form(u[e], x2);
-        d[e] *= __builtin_fmaf(u[e] * s * (1.0f - s), kTanhK * __builtin_fmaf(3.0f * kTanhC, x2, 1.0f), s);
-      }
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float s = logistic2(u[e] * -kLog2);
-        d[e] *= __builtin_fmaf(u[e] * s, 1.0f - s, s);
-      }
-      break;
-    default: break;
+    case kActRelu: f(std::integral_constant<int, kActRelu>()); break;
+    case kActRelu2: f(std::integral_constant<int, kActRelu2>()); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>()); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>()); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>()); break;
+    default: f(std::integral_constant<int, kActNone>()); break;
   }
 }
 
