@@ -607,13 +607,19 @@ enum {
  *   residual  in   fp16 [T, R], or NULL
  *   U         out  fp16 [T, R], or NULL
  *   Y         out  fp16 [T, R]; may be the residual's own memory
+ *   workspace scratch device memory of sp24_spmm_fwd_act_workspace bytes (NULL
+ *             where those are 0)
  * U of +inf gives +inf; of -inf 0 with RELU, RELU2 and GELU, NaN with GELU_TANH
  * and SILU (-inf * 0); NaN gives NaN.
- * Errors: NULL, SHAPE, ALIGN, LAUNCH; UNSUPPORTED for another act; TOO_LARGE as
- * for sp24_spmm_fwd, and when R reaches 2^27.
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, LAUNCH; UNSUPPORTED for another act;
+ * TOO_LARGE as for sp24_spmm_fwd, and when R reaches 2^27.
  */
 int sp24_spmm_fwd_act(const void* X, const void* vals_row, const uint16_t* meta_row, int64_t T, int64_t R, int64_t C,
-                      const float* bias, int act, const void* residual, void* U, void* Y, void* stream);
+                      const float* bias, int act, const void* residual, void* U, void* Y, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
+/* Host only: the workspace bytes of such a call; -1 for sizes it refuses. */
+int64_t sp24_spmm_fwd_act_workspace(int64_t T, int64_t R, int64_t C);
 
 /*
  * Input-gradient 2:4 sparse GEMM through the activation before the layer, with
@@ -633,8 +639,8 @@ int sp24_spmm_fwd_act(const void* X, const void* vals_row, const uint16_t* meta_
  *   dU        out  fp16 [T, C]; may be U's own memory
  *   dbias     out  fp32 [C], or NULL.  Written, not accumulated (zeros if T is 0).
  *   workspace scratch device memory of sp24_spmm_bwd_input_act_workspace bytes
- *             (NULL where those are 0, or without dbias)
- * Errors: as sp24_spmm_fwd_act (C reaching 2^27), and WORKSPACE.
+ *             (NULL where those are 0)
+ * Errors: as sp24_spmm_fwd_act (C reaching 2^27).
  */
 int sp24_spmm_bwd_input_act(const void* dY, const void* vals_col, const uint16_t* meta_col, int64_t T, int64_t R,
                             int64_t C, int act, const void* U, void* dU, float* dbias, void* workspace,

@@ -174,6 +174,12 @@ int check_spmm_act(const void* A, const void* vals, const uint16_t* meta, int64_
   return st == SP24_OK && N >= kMaxActFeatures ? SP24_ERR_TOO_LARGE : st;
 }
 
+// Whether a product's sizes alone are taken (no pointer is looked at with T = 0).
+bool act_sizes(int64_t T, int64_t N, int64_t K) {
+  return check_spmm_act(nullptr, nullptr, nullptr, 0, N, K, 0, nullptr) == SP24_OK && T >= 0 && T < kMaxDim &&
+         (T == 0 || (K < kMaxElems / T && N < kMaxElems / T));
+}
+
 // A call's workspace of `need` bytes.
 int check_workspace(const void* workspace, int64_t workspace_bytes, int64_t need) {
   if (need == 0) return SP24_OK;
@@ -488,22 +494,25 @@ int sp24_muon_step(const sp24_muon_job* jobs, int count, float momentum, int nes
 }
 
 int sp24_spmm_fwd_act(const void* X, const void* vals_row, const uint16_t* meta_row, int64_t T, int64_t R, int64_t C,
-                      const float* bias, int act, const void* residual, void* U, void* Y, void* stream) {
+                      const float* bias, int act, const void* residual, void* U, void* Y, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
   static_assert((int)SP24_ACT_SILU == (int)sp24::kActSilu && (int)SP24_ACT_GELU == (int)sp24::kActGelu, "activations");
-  const int st = check_spmm_act(X, vals_row, meta_row, T, R, C, act, Y);
+  int st = check_spmm_act(X, vals_row, meta_row, T, R, C, act, Y);
   if (st != SP24_OK || T == 0 || R == 0) return st;
   if ((bias && !aligned16(bias)) || (residual && !aligned16(residual)) || (U && !aligned16(U))) return SP24_ERR_ALIGN;
+  if ((st = check_workspace(workspace, workspace_bytes, sp24::spmm_act_fwd_workspace(T, R, C))) != SP24_OK) return st;
   return launch_status(sp24::launch_spmm_act_fwd(
       static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(vals_row), meta_row, T, R, C, bias, act,
-      static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(U), static_cast<uint16_t*>(Y), as_stream(stream)));
+      static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(U), static_cast<uint16_t*>(Y), workspace,
+      as_stream(stream)));
+}
+
+int64_t sp24_spmm_fwd_act_workspace(int64_t T, int64_t R, int64_t C) {
+  return act_sizes(T, R, C) ? sp24::spmm_act_fwd_workspace(T, R, C) : -1;
 }
 
 int64_t sp24_spmm_bwd_input_act_workspace(int64_t T, int64_t R, int64_t C) {
-  // sizes alone: no pointer is looked at with T = 0
-  if (check_spmm(nullptr, nullptr, nullptr, 0, C, R, nullptr) != SP24_OK || C >= kMaxActFeatures || T < 0 ||
-      T >= kMaxDim || (T != 0 && (R >= kMaxElems / T || C >= kMaxElems / T)))
-    return -1;
-  return sp24::spmm_act_bwd_workspace(T, C);
+  return act_sizes(T, C, R) ? sp24::spmm_act_bwd_workspace(T, C, R, true) : -1;
 }
 
 int sp24_spmm_bwd_input_act(const void* dY, const void* vals_col, const uint16_t* meta_col, int64_t T, int64_t R,
@@ -515,8 +524,8 @@ int sp24_spmm_bwd_input_act(const void* dY, const void* vals_col, const uint16_t
   if (T != 0) {
     if (act != SP24_ACT_NONE && U == nullptr) return SP24_ERR_NULL;
     if (U && !aligned16(U)) return SP24_ERR_ALIGN;
-    if (dbias && (st = check_workspace(workspace, workspace_bytes, sp24::spmm_act_bwd_workspace(T, C))) != SP24_OK)
-      return st;
+    st = check_workspace(workspace, workspace_bytes, sp24::spmm_act_bwd_workspace(T, C, R, dbias != nullptr));
+    if (st != SP24_OK) return st;
   }
   return launch_status(sp24::launch_spmm_act_bwd(static_cast<const uint16_t*>(dY), static_cast<const uint16_t*>(vals_col),
                                                  meta_col, T, C, R, act, static_cast<const uint16_t*>(U),

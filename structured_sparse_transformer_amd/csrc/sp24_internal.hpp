@@ -149,13 +149,15 @@ hipError_t launch_newton_schulz(const NsJob* jobs, int count, const NsParams& pr
 enum { kActNone = 0, kActRelu, kActRelu2, kActGelu, kActGeluTanh, kActSilu, kActCount };
 
 // U = X S^T + bias, Y = act(U) + residual; bias, residual and U may be null.
-// X [T][K], S's forms as launch_spmm_nt takes them, the others [T][N].
+// X [T][K], S's forms as launch_spmm_nt takes them, the others [T][N].  ws:
+// spmm_act_fwd_workspace bytes.
+int64_t spmm_act_fwd_workspace(int64_t T, int64_t N, int64_t K);
 hipError_t launch_spmm_act_fwd(const uint16_t* X, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N,
                                int64_t K, const float* bias, int act, const uint16_t* residual, uint16_t* U,
-                               uint16_t* Y, hipStream_t s);
+                               uint16_t* Y, void* ws, hipStream_t s);
 // dU = (dY S^T) * act'(U) and, unless dbias is null, its sums over tokens.  ws:
-// spmm_act_bwd_workspace bytes (none needed without dbias).
-int64_t spmm_act_bwd_workspace(int64_t T, int64_t N);
+// spmm_act_bwd_workspace bytes (`sums`: with dbias).
+int64_t spmm_act_bwd_workspace(int64_t T, int64_t N, int64_t K, bool sums);
 hipError_t launch_spmm_act_bwd(const uint16_t* dY, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N,
                                int64_t K, int act, const uint16_t* U, uint16_t* dU, float* dbias, void* ws,
                                hipStream_t s);

@@ -36,6 +36,42 @@ struct Finish {
   int act;
 };
 
+// What a kernel makes of its sums: kPartial leaves them as they are.
+enum { kForward, kBackward, kPartial };
+
+// A lane's 4 consecutive features of one token, from element `at` of the
+// matrices and feature f.
+template <bool kBwd>
+__device__ __forceinline__ void finish4(const Finish& fin, int64_t at, int64_t f, float (&d)[4]) {
+  if constexpr (kBwd) {
+    if (fin.act != kActNone) {
+      const h4 u = *reinterpret_cast<const h4*>(fin.u_in + at);
+      with_act(fin.act, [&](auto kind) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = times_slope<decltype(kind)::value>(d[e], (float)u[e]);
+      });
+    }
+  } else {
+    if (fin.bias != nullptr) {
+      const float4v bias = *reinterpret_cast<const float4v*>(fin.bias + f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] += bias[e];
+    }
+    if (fin.u_out != nullptr)
+      *reinterpret_cast<h4*>(fin.u_out + at) = h4{(_Float16)d[0], (_Float16)d[1], (_Float16)d[2], (_Float16)d[3]};
+    with_act(fin.act, [&](auto kind) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = activate<decltype(kind)::value>(d[e]);
+    });
+    if (fin.add != nullptr) {
+      const h4 r = *reinterpret_cast<const h4*>(fin.add + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] += (float)r[e];
+    }
+  }
+  *reinterpret_cast<h4*>(fin.out + at) = h4{(_Float16)d[0], (_Float16)d[1], (_Float16)d[2], (_Float16)d[3]};
+}
+
 // ---------------------------------------------------------------------------
 // Products of few tokens.
 //
@@ -108,19 +144,10 @@ __global__ __launch_bounds__(64 * WAVES) void spmm_thin_kernel(const uint16_t* _
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] += p[e];
     }
-    const int64_t t = t0 + nt * 16 + l16, at = t * N + f0 + 4 * g;
+    const int64_t t = t0 + nt * 16 + l16;
     const bool real = t < T;
-    if constexpr (kBwd) {
-      if (real) {
-        if (fin.act != kActNone) {
-          const h4 u = *reinterpret_cast<const h4*>(fin.u_in + at);
-          with_act(fin.act, [&](auto kind) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = times_slope<decltype(kind)::value>(d[e], (float)u[e]);
-          });
-        }
-        *reinterpret_cast<h4*>(fin.out + at) = h4{(_Float16)d[0], (_Float16)d[1], (_Float16)d[2], (_Float16)d[3]};
-      }
+    if (real) finish4<kBwd>(fin, t * N + f0 + 4 * g, f0 + 4 * g, d);
+    if constexpr (kBwd)
       if (fin.sums != nullptr) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -130,25 +157,6 @@ __global__ __launch_bounds__(64 * WAVES) void spmm_thin_kernel(const uint16_t* _
           if (l16 == 0) colsum[nt][g][e] = v;
         }
       }
-    } else if (real) {
-      if (fin.bias != nullptr) {
-        const float4v bias = *reinterpret_cast<const float4v*>(fin.bias + f0 + 4 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] += bias[e];
-      }
-      if (fin.u_out != nullptr)
-        *reinterpret_cast<h4*>(fin.u_out + at) = h4{(_Float16)d[0], (_Float16)d[1], (_Float16)d[2], (_Float16)d[3]};
-      with_act(fin.act, [&](auto kind) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = activate<decltype(kind)::value>(d[e]);
-      });
-      if (fin.add != nullptr) {
-        const h4 r = *reinterpret_cast<const h4*>(fin.add + at);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] += (float)r[e];
-      }
-      *reinterpret_cast<h4*>(fin.out + at) = h4{(_Float16)d[0], (_Float16)d[1], (_Float16)d[2], (_Float16)d[3]};
-    }
   }
   if constexpr (kBwd) {
     __syncthreads();
@@ -205,11 +213,11 @@ hipError_t launch_thin(const uint16_t* A, const uint16_t* vals, const uint16_t* 
 // the first half of its 512 bytes and the odd ones in the second, each half
 // XOR-swizzled by the token, so that 8 lanes that write one chunk of 8 tokens,
 // and 16 that read 16 chunks of one, meet no bank twice.
-template <int BM, int BN, int WM, int WN, bool kBwd, bool kTail>
+template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
 __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, const uint16_t* __restrict__ A,
                                               const uint16_t* __restrict__ vals, const uint16_t* __restrict__ meta,
                                               int64_t T, int64_t N, int64_t K, int tm, int tn, int tid,
-                                              const Finish& fin, int64_t ld, int64_t t0) {
+                                              const Finish& fin, int64_t t0) {
 #include "sp24_spmm_loop.inc"
 
   if constexpr (kTail) {
@@ -265,9 +273,9 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
   const uint16_t* const beside = kBwd ? fin.u_in : fin.add;
   h8 next[8];
   const int first = lane >> 4, last = (int)T - 1;
-  const uint16_t* const from_m = beside + t0 * ld + (inside ? m : 0);
+  const uint16_t* const from_m = beside + t0 * N + (inside ? m : 0);
   const auto fetch = [&](int pass) {
-    return *reinterpret_cast<const h8*>(from_m + (int64_t)min(wn * WN + pass * 4 + first, last) * ld);
+    return *reinterpret_cast<const h8*>(from_m + (int64_t)min(wn * WN + pass * 4 + first, last) * N);
   };
   if (beside != nullptr)
 #pragma unroll
@@ -296,7 +304,7 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
         if (beside != nullptr && nt + 1 < Cfg::TN) next[it] = fetch((nt + 1) * 8 + it);
         const int n = wn * WN + nt * 32 + t;
         if (n > last || !inside) continue;
-        const int64_t at = (t0 + n) * ld + m;
+        const int64_t at = (t0 + n) * N + m;
         float d[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         if constexpr (kBwd) {
 #pragma unroll
@@ -344,17 +352,17 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < Cfg::WAVES_N; ++w) v += all[w * BM + c];
-      if (m0 + c < N) fin.sums[t0 / BN * ld + m0 + c] = v;
+      if (m0 + c < N) fin.sums[t0 / BN * N + m0 + c] = v;
     }
   }
 }
 
-template <int BM, int BN, int WM, int WN, bool kBwd, bool kTail>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void spmm_act_kernel(
+template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void spmm_act_kernel(
     const uint16_t* __restrict__ A, const uint16_t* __restrict__ vals, const uint16_t* __restrict__ meta, int64_t T,
-    int64_t N, int64_t K, Finish fin, int64_t ld, int tiles_m, int tiles_n) {
+    int64_t N, int64_t K, Finish fin, int tiles_m, int tiles_n) {
   using Cfg = FastCfg<BM, BN, WM, WN>;
-  __shared__ __align__(1024) unsigned char smem[3 * (Cfg::S_BYTES + Cfg::B_BYTES + Cfg::M_BYTES)];
+  __shared__ __align__(1024) unsigned char smem[kSlots * (Cfg::S_BYTES + Cfg::B_BYTES + Cfg::M_BYTES)];
   static_assert(WM == 128 && WN % 32 == 0 && Cfg::WAVES * 16384 <= sizeof(smem), "staging");
 
   // tile order as in the products alone: groups of 8 feature tiles, token tiles
@@ -371,78 +379,301 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 1) void spmm_act_kernel
   // the tile's tokens as a matrix of their own, so that the direct loads' 32-bit
   // offsets count from its first row however many tokens there are
   const int64_t t0 = (int64_t)tn * BN;
-  spmm_act_tile<BM, BN, WM, WN, kBwd, kTail>(smem, A + t0 * K, vals, meta, T - t0 < BN ? T - t0 : BN, N, K, tm, 0,
-                                             (int)threadIdx.x, fin, ld, t0);
+  spmm_act_tile<BM, BN, WM, WN, kSlots, kBwd, kTail>(smem, A + t0 * K, vals, meta, T - t0 < BN ? T - t0 : BN, N, K, tm, 0,
+                                                     (int)threadIdx.x, fin, t0);
 }
 
-// Features [m, m + n) of a product over N, for all tokens.
-template <int BM, int BN, int WM, int WN, bool kBwd>
+template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd>
 hipError_t launch_tiles(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
-                        Finish f, int64_t m, int64_t n, hipStream_t s) {
-  const int tiles_m = (int)((n + BM - 1) / BM), tiles_n = (int)((T + BN - 1) / BN);
+                        const Finish& f, hipStream_t s) {
+  const int tiles_m = (int)((N + BM - 1) / BM), tiles_n = (int)((T + BN - 1) / BN);
   const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8)), block(FastCfg<BM, BN, WM, WN>::THREADS);
-  vals += m * (K / 2);   // m is a multiple of 64: a band's start
-  meta += m * (K / 16);
-  if (f.bias) f.bias += m;
-  if (f.add) f.add += m;
-  if (f.u_in) f.u_in += m;
-  if (f.u_out) f.u_out += m;
-  if (f.sums) f.sums += m;
-  f.out += m;
   if (K % 64 == 0)
-    hipLaunchKernelGGL((spmm_act_kernel<BM, BN, WM, WN, kBwd, false>), grid, block, 0, s, A, vals, meta, T, n, K, f, N,
+    hipLaunchKernelGGL((spmm_act_kernel<BM, BN, WM, WN, kSlots, kBwd, false>), grid, block, 0, s, A, vals, meta, T, N, K, f,
                        tiles_m, tiles_n);
   else
-    hipLaunchKernelGGL((spmm_act_kernel<BM, BN, WM, WN, kBwd, true>), grid, block, 0, s, A, vals, meta, T, n, K, f, N,
+    hipLaunchKernelGGL((spmm_act_kernel<BM, BN, WM, WN, kSlots, kBwd, true>), grid, block, 0, s, A, vals, meta, T, N, K, f,
                        tiles_m, tiles_n);
   return hipGetLastError();
 }
 
-// The most tokens that run without tiles.
-constexpr int64_t kMostThin = 64;
+// ---------------------------------------------------------------------------
+// Products whose tiles are too few for the CUs: 64 features x 64 tokens a
+// workgroup, and the reduction shared out inside it.
+//
+// A long reduction over few tiles is a chain of stages, each of which waits for
+// its operands, the LDS and the matrix unit in turn (0.4 us a stage of 64 in the
+// tiles above), on a part of the CUs.  Here a workgroup of 16 waves has four
+// groups of four; group k sums up the stages k, k + 4, k + 8, ... of the whole
+// tile, 32 x 32 a wave, through a ring of its own, so that four stages are under
+// way in each CU and a quarter as many follow one another; and the tiles are a
+// quarter as large.  The four sums meet in LDS, in order.
+//
+// With few tokens there are too few tiles even so, and a CU's loads are the
+// bound (51 KB a round of stages in 0.47 us, 52 bytes a cycle): `parts`
+// workgroups share a tile's reduction then (kPartial), part p the stages
+// [p n / parts, (p + 1) n / parts), the last one the tail too, into
+// fin.sums + p T N, and join_parts_kernel finishes.
+template <int kMode, bool kTail>
+__global__ __launch_bounds__(1024, 1) void spmm_mid_kernel(const uint16_t* __restrict__ A,
+                                                           const uint16_t* __restrict__ vals,
+                                                           const uint16_t* __restrict__ meta, int64_t T, int64_t N,
+                                                           int64_t K, Finish fin, int tiles_m, int tiles_n, int parts) {
+  constexpr int kStage = 4096 + 8192 + 512, kSlots = 3;   // S, A and meta of 64 x 64 in K
+  __shared__ __align__(1024) unsigned char smem[4 * kSlots * kStage];
+  const int all = tiles_m * tiles_n * parts, per_xcd = (all + 7) / 8;
+  const int lin = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+  if (lin >= all) return;
+  // an XCD's tiles share their strip of S
+  const int tn = __builtin_amdgcn_readfirstlane(lin % tiles_n), strip = lin / tiles_n;
+  const int part = __builtin_amdgcn_readfirstlane(strip % parts), tm = __builtin_amdgcn_readfirstlane(strip / parts);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = wave >> 2, w = wave & 3, wm = w & 1, wn = w >> 1, l32 = lane & 31, g = lane >> 5;
+  const int64_t m0 = (int64_t)tm * 64, t0 = (int64_t)tn * 64;
+  const int64_t h = min<int64_t>(64, N - m0), tokens = min<int64_t>(64, T - t0);
+  const int all_n = (int)(K / 64), first = part * all_n / parts, n = (part + 1) * all_n / parts - first;
+  const int mine = (n - kg + 3) / 4, rounds = (n + 3) / 4;
 
-// Whether the tiles take a product: its 32-bit offsets reach 256 rows of A and
-// all of S, and a launch counts its work-items in 32 bits.
-bool in_tiles(int64_t T, int64_t N, int64_t K) {
-  constexpr int64_t kMaxBuf = (int64_t)1 << 31;
-  return T > kMostThin && K >= 64 && K * 512 < kMaxBuf && N * K < kMaxBuf &&
-         ((T + 63) / 64) * ((N + 127) / 128) < ((int64_t)1 << 22);
+  // direct loads as in the tiles above: rows past T read as zero, rows past N
+  // read zero or other rows of S and feed outputs that are not stored
+  const i32x4 rs = make_rsrc(vals + m0 * (K / 2), (uint32_t)((N - m0) * K));
+  const i32x4 rb = make_rsrc(A + t0 * K, (uint32_t)(tokens * K * 2));
+  const i32x4 rm = make_rsrc(meta + m0 * (K / 16), (uint32_t)((N - m0) * (K / 8)));
+  const int st_s = (int)h * 64, st_m = (int)h * 8;
+  const int rs_row = 16 * w + lane / 4, rm_row = 32 * (w & 1) + lane / 2;
+  const int off_s = rs_row * 64 + (((lane % 4) ^ swz_s(rs_row)) * 16), off_m = rm_row * 8 + (lane % 2) * 4;
+  int off_b[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * (2 * w + i) + lane / 8;
+    off_b[i] = r * (int)K * 2 + (((lane % 8) ^ swz_b(r)) * 16);
+  }
+  unsigned char* const ring = smem + kg * (kSlots * kStage);
+  const auto issue = [&](int j) {   // this group's j-th stage: 4 loads a wave
+    const int kt = first + kg + 4 * j;
+    const uint32_t to = lds_addr(ring + (j % kSlots) * kStage);
+    dma_b128(rs, to + w * 1024, off_s + kt * st_s);
+    dma_b128(rb, to + 4096 + (2 * w) * 1024, off_b[0] + kt * 128);
+    dma_b128(rb, to + 4096 + (2 * w + 1) * 1024, off_b[1] + kt * 128);
+    // both pairs of waves load the 512 bytes of meta: the waits count alike
+    dma_b32(rm, to + 12288 + (w & 1) * 256, off_m + kt * st_m);
+  };
+  int rd_s[2], rd_b[2][2];
+#pragma unroll
+  for (int st = 0; st < 2; ++st) {
+    rd_s[st] = (wm * 32 + l32) * 64 + (((2 * st + g) ^ swz_s(l32)) * 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rd_b[st][i] = 4096 + (wn * 32 + l32) * 128 + (((4 * st + 2 * i + g) ^ swz_b(l32)) * 16);
+  }
+  const int rd_m = 12288 + (wm * 32 + l32) * 8;
+  f16v acc;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+
+  // Stage j is issued two rounds ahead, into the slot that round j - 3 read:
+  // every wave is past the barrier of round j - 2 then.
+  if (mine > 0) issue(0);
+  if (mine > 1) issue(1);
+  for (int j = 0; j < rounds; ++j) {
+    // stage j has landed (the next one's 4 loads may be under way); vmcnt in
+    // bits 3:0, no wait for others
+    if (j + 1 < mine) __builtin_amdgcn_s_waitcnt(4 | (7 << 4) | (15 << 8));
+    else __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (j >= mine) continue;
+    if (j + 2 < mine) issue(j + 2);
+    const unsigned char* const from = ring + (j % kSlots) * kStage;
+    const uint2 mw = *reinterpret_cast<const uint2*>(from + rd_m);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const h8 a = *reinterpret_cast<const h8*>(from + rd_s[st]);
+      const h8 lo = *reinterpret_cast<const h8*>(from + rd_b[st][0]);
+      const h8 hi = *reinterpret_cast<const h8*>(from + rd_b[st][1]);
+      const h16 b = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+      const uint32_t word = st ? mw.y : mw.x;
+      acc = __builtin_amdgcn_smfmac_f32_32x32x32_f16(a, b, acc, (int)(g ? word >> 16 : word), 0, 0);
+    }
+  }
+  if constexpr (kTail) {
+    if (kg == 0 && part + 1 == parts) {
+      // the last 16, 32 or 48 of the reduction, as in the tiles above
+      const int64_t k0 = K / 64 * 64;
+      const int left = (int)(K - k0);
+      const int64_t row = min<int64_t>(wm * 32 + l32, h - 1), token = min<int64_t>(wn * 32 + l32, tokens - 1);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int c = 2 * st + g;
+        h8 a = {}, lo = {}, hi = {};
+        int idx = 0;
+        if (16 * c < left) {
+          a = *reinterpret_cast<const h8*>(vals + m0 * (K / 2) + k0 / 2 * h + row * (left / 2) + 8 * c);
+          idx = meta[m0 * (K / 16) + k0 / 16 * h + row * (left / 16) + c];
+        }
+        const uint16_t* const x = A + (t0 + token) * K + k0 + 32 * st + 8 * g;
+        if (32 * st + 8 * g < left) lo = *reinterpret_cast<const h8*>(x);
+        if (32 * st + 16 + 8 * g < left) hi = *reinterpret_cast<const h8*>(x + 16);
+        const h16 b = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15);
+        acc = __builtin_amdgcn_smfmac_f32_32x32x32_f16(a, b, acc, idx, 0, 0);
+      }
+    }
+  }
+  __syncthreads();   // no wave reads the rings any more
+  // sums of the groups, [4][64 tokens][16 chunks of 4 features, XOR-swizzled]
+#pragma unroll
+  for (int i4 = 0; i4 < 4; ++i4) {
+    const int t = wn * 32 + l32, c = wm * 8 + 2 * i4 + g;
+    *reinterpret_cast<float4v*>(smem + kg * 16384 + t * 256 + ((c ^ (t & 15)) * 16)) =
+        float4v{acc[4 * i4], acc[4 * i4 + 1], acc[4 * i4 + 2], acc[4 * i4 + 3]};
+  }
+  __syncthreads();
+  const int t = threadIdx.x >> 4, quad = threadIdx.x & 15;
+  const int64_t f = m0 + 4 * quad;
+  const bool real = t < tokens && f < N;
+  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (real) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4v p = *reinterpret_cast<const float4v*>(smem + k * 16384 + t * 256 + ((quad ^ (t & 15)) * 16));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] += p[e];
+    }
+    const int64_t at = (t0 + t) * N + f;
+    if constexpr (kMode == kPartial)
+      *reinterpret_cast<float4v*>(fin.sums + part * T * N + at) = float4v{d[0], d[1], d[2], d[3]};
+    else
+      finish4<kMode == kBackward>(fin, at, f, d);
+  }
+  if constexpr (kMode == kBackward) {
+    if (fin.sums == nullptr) return;   // the same in all lanes
+    float* const all = reinterpret_cast<float*>(smem + 65536);   // [16 waves][64]
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d[e] += __shfl_xor(d[e], 16);
+      d[e] += __shfl_xor(d[e], 32);
+    }
+    if (lane < 16) *reinterpret_cast<float4v*>(all + wave * 64 + 4 * quad) = float4v{d[0], d[1], d[2], d[3]};
+    __syncthreads();
+    if (threadIdx.x < 64 && m0 + (int)threadIdx.x < N) {
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += all[k * 64 + threadIdx.x];
+      fin.sums[(int64_t)tn * N + m0 + threadIdx.x] = v;
+    }
+  }
 }
 
-// A backward's partial sums: features below `features` have a row for each
-// `first` tokens, the others one for each `rest`.
-struct Blocks {
-  int64_t features, first, rest;
+template <int kMode>
+hipError_t launch_mid(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
+                      const Finish& f, int parts, hipStream_t s) {
+  const int tiles_m = (int)((N + 63) / 64), tiles_n = (int)((T + 63) / 64);
+  const dim3 grid((unsigned)((tiles_m * tiles_n * parts + 7) / 8 * 8)), block(1024);
+  if (K % 64 == 0)
+    hipLaunchKernelGGL((spmm_mid_kernel<kMode, false>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n, parts);
+  else
+    hipLaunchKernelGGL((spmm_mid_kernel<kMode, true>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n, parts);
+  return hipGetLastError();
+}
+
+// Joins the parts of a product's sums, part[parts][T][N], in order, and finishes
+// them: a workgroup has 16 tokens x 64 features, a lane 4 features of a token.
+constexpr int kJoinTokens = 16;
+template <bool kBwd>
+__global__ __launch_bounds__(256) void join_parts_kernel(const float* __restrict__ part, int parts, int64_t T, int64_t N,
+                                                         Finish fin) {
+  __shared__ float4v col[16][16];
+  const int quad = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const int64_t f = (int64_t)blockIdx.x * 64 + 4 * quad, t = (int64_t)blockIdx.y * kJoinTokens + row;
+  const bool real = t < T && f < N;
+  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (real) {
+    const int64_t at = t * N + f;
+    for (int p = 0; p < parts; p += 8) {
+      float4v x[8];   // eight parts under way at once
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (p + k < parts) x[k] = *reinterpret_cast<const float4v*>(part + (p + k) * T * N + at);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (p + k < parts)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] += x[k][e];
+    }
+    finish4<kBwd>(fin, at, f, d);
+  }
+  if constexpr (kBwd) {
+    if (fin.sums == nullptr) return;   // the same in all lanes
+    col[row][quad] = real ? float4v{d[0], d[1], d[2], d[3]} : float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    if (row != 0 || f >= N) return;
+    float4v v = col[0][quad];
+#pragma unroll
+    for (int r = 1; r < 16; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += col[r][quad][e];
+    *reinterpret_cast<float4v*>(fin.sums + blockIdx.y * N + f) = v;
+  }
+}
+
+// How a product is run, by its sizes alone: the order of its sums does not depend
+// on the device.
+struct Plan {
+  enum { kThin, kMid, kSmall, kLarge } how;
+  int parts;       // of kMid
+  int64_t block;   // tokens of one row of a backward's partial sums
+  int64_t rows(int64_t T) const { return (T + block - 1) / block; }
+  int64_t part_floats(int64_t T, int64_t N) const { return parts > 1 ? parts * T * N : 0; }
 };
 
+Plan plan_product(int64_t T, int64_t N, int64_t K) {
+  constexpr int64_t kCus = 256;   // of an MI355X
+  const auto tiles = [&](int64_t features, int64_t tokens) {
+    return ((T + tokens - 1) / tokens) * ((N + features - 1) / features);
+  };
+  // the tiles' 32-bit offsets reach 256 rows of A and all of S, and a launch
+  // counts its work-items in 32 bits
+  constexpr int64_t kMaxBuf = (int64_t)1 << 31;
+  const bool fits = K >= 64 && K * 512 < kMaxBuf && N * K < kMaxBuf && tiles(64, 64) < ((int64_t)1 << 22);
+  if (!fits || T <= 16 || (T <= 32 && K <= 1024)) return {Plan::kThin, 1, T <= 16 ? 16 : T <= 32 ? 32 : kThinTokens};
+  if (2 * tiles(64, 64) <= 3 * kCus) {
+    const int64_t rounds = (K / 64 + 3) / 4, parts = std::min(kCus / tiles(64, 64), rounds / 2);
+    // the joining launch costs about 3 us, a round 0.47
+    if (parts > 1 && rounds - (rounds + parts - 1) / parts >= 7) return {Plan::kMid, (int)parts, kJoinTokens};
+    return {Plan::kMid, 1, 64};
+  }
+  return {tiles(256, 128) < 2 * kCus ? Plan::kSmall : Plan::kLarge, 1, 128};
+}
+
 template <bool kBwd>
-hipError_t launch_product(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
-                          const Finish& fin, Blocks* blocks, hipStream_t s) {
-  if (!in_tiles(T, N, K)) {
-    *blocks = {N, T <= 16 ? 16 : T <= 32 ? 32 : kThinTokens, kThinTokens};
-    return launch_thin<kBwd>(A, vals, meta, T, N, K, fin, s);
+hipError_t launch_product(const Plan& p, const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T,
+                          int64_t N, int64_t K, const Finish& fin, float* ws, hipStream_t s) {
+  switch (p.how) {
+    case Plan::kThin: return launch_thin<kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kSmall: return launch_tiles<128, 128, 128, 32, 3, kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kLarge: return launch_tiles<256, 128, 128, 64, 2, kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kMid: break;
   }
-  const int64_t cus = device_cu_count(), tiles = ((T + 255) / 256) * ((N + 255) / 256);
-  if (tiles < cus) {
-    *blocks = {N, 128, 128};
-    return launch_tiles<128, 128, 128, 32, kBwd>(A, vals, meta, T, N, K, fin, 0, N, s);
-  }
-  *blocks = {N, 256, 256};
-  return launch_tiles<256, 256, 128, 64, kBwd>(A, vals, meta, T, N, K, fin, 0, N, s);
+  if (p.parts == 1) return launch_mid<kBwd ? kBackward : kForward>(A, vals, meta, T, N, K, fin, 1, s);
+  Finish part{};
+  part.sums = ws;
+  const hipError_t e = launch_mid<kPartial>(A, vals, meta, T, N, K, part, p.parts, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(join_parts_kernel<kBwd>, dim3((unsigned)((N + 63) / 64), (unsigned)p.rows(T)), dim3(256), 0, s, ws,
+                     p.parts, T, N, fin);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Sums over rows.
 
-// out[c] = the sum of part[P][N]'s rows: P rows for columns below `split` (a
-// multiple of 64), Q for the others.  Eight waves take every eighth row, eight
+// out[c] = the sum of part[P][N]'s rows.  Eight waves take every eighth row, eight
 // rows at a time, of 64 columns, and their sums are added in order.
-__global__ __launch_bounds__(512) void join_rows_kernel(const float* __restrict__ part, int64_t P, int64_t split,
-                                                        int64_t Q, int64_t N, float* __restrict__ out) {
+__global__ __launch_bounds__(512) void join_rows_kernel(const float* __restrict__ part, int64_t P, int64_t N,
+                                                        float* __restrict__ out) {
   __shared__ float waves[8][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  if (c - lane >= split) P = Q;
   float v = 0.0f;
   if (c < N)
     for (int64_t p = wave; p < P; p += 64) {
@@ -460,9 +691,8 @@ __global__ __launch_bounds__(512) void join_rows_kernel(const float* __restrict_
   out[c] = v;
 }
 
-hipError_t launch_join_rows(const float* part, int64_t P, int64_t split, int64_t Q, int64_t N, float* out,
-                            hipStream_t s) {
-  hipLaunchKernelGGL(join_rows_kernel, dim3((unsigned)((N + 63) / 64)), dim3(512), 0, s, part, P, split, Q, N, out);
+hipError_t launch_join_rows(const float* part, int64_t P, int64_t N, float* out, hipStream_t s) {
+  hipLaunchKernelGGL(join_rows_kernel, dim3((unsigned)((N + 63) / 64)), dim3(512), 0, s, part, P, N, out);
   return hipGetLastError();
 }
 
@@ -516,21 +746,25 @@ hipError_t launch_bias_grad(const uint16_t* dY, int64_t T, int64_t R, float* out
                      part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || P == 1) return e;
-  return launch_join_rows(part, P, R, P, R, out, s);
+  return launch_join_rows(part, P, R, out, s);
+}
+
+int64_t spmm_act_fwd_workspace(int64_t T, int64_t N, int64_t K) {
+  return T == 0 || N == 0 ? 0 : 4 * plan_product(T, N, K).part_floats(T, N);
 }
 
 hipError_t launch_spmm_act_fwd(const uint16_t* X, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N,
                                int64_t K, const float* bias, int act, const uint16_t* residual, uint16_t* U,
-                               uint16_t* Y, hipStream_t s) {
+                               uint16_t* Y, void* ws, hipStream_t s) {
   if (T == 0 || N == 0) return hipSuccess;
   const Finish fin{bias, residual, nullptr, U, Y, nullptr, act};
-  Blocks blocks;
-  return launch_product<false>(X, vals, meta, T, N, K, fin, &blocks, s);
+  return launch_product<false>(plan_product(T, N, K), X, vals, meta, T, N, K, fin, static_cast<float*>(ws), s);
 }
 
-int64_t spmm_act_bwd_workspace(int64_t T, int64_t N) {
-  const int64_t P = (T + kThinTokens - 1) / kThinTokens;
-  return P > 1 ? P * N * 4 : 0;
+int64_t spmm_act_bwd_workspace(int64_t T, int64_t N, int64_t K, bool sums) {
+  if (T == 0 || N == 0) return 0;
+  const Plan p = plan_product(T, N, K);
+  return 4 * (p.part_floats(T, N) + (sums && p.rows(T) > 1 ? p.rows(T) * N : 0));
 }
 
 hipError_t launch_spmm_act_bwd(const uint16_t* dY, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N,
@@ -538,13 +772,13 @@ hipError_t launch_spmm_act_bwd(const uint16_t* dY, const uint16_t* vals, const u
                                hipStream_t s) {
   if (N == 0) return hipSuccess;
   if (T == 0) return dbias ? launch_bias_grad(nullptr, 0, N, dbias, nullptr, s) : hipSuccess;
-  const int64_t P = (T + kThinTokens - 1) / kThinTokens;
-  float* sums = dbias == nullptr ? nullptr : P > 1 ? static_cast<float*>(ws) : dbias;
+  const Plan p = plan_product(T, N, K);
+  float* const parts = static_cast<float*>(ws);
+  float* const sums = dbias == nullptr ? nullptr : p.rows(T) > 1 ? parts + p.part_floats(T, N) : dbias;
   const Finish fin{nullptr, nullptr, act == kActNone ? nullptr : U, nullptr, dU, sums, act};
-  Blocks b;
-  const hipError_t e = launch_product<true>(dY, vals, meta, T, N, K, fin, &b, s);
-  if (e != hipSuccess || sums == nullptr || P == 1) return e;
-  return launch_join_rows(sums, (T + b.first - 1) / b.first, b.features, (T + b.rest - 1) / b.rest, N, dbias, s);
+  const hipError_t e = launch_product<true>(p, dY, vals, meta, T, N, K, fin, parts, s);
+  if (e != hipSuccess || sums == nullptr || p.rows(T) == 1) return e;
+  return launch_join_rows(sums, p.rows(T), N, dbias, s);
 }
 
 }  // namespace sp24

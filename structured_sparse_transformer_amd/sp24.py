@@ -33,7 +33,7 @@ EXPORTS = ("sp24_mask_search", "sp24_compress", "sp24_search_compress", "sp24_se
            "sp24_spmm_fwd", "sp24_spmm_fwd_geglu", "sp24_spmm_bwd_input", "sp24_spmm_group",
            "sp24_spmm_group_noalloc", "sp24_embed_fwd", "sp24_embed_bwd", "sp24_embed_bwd_workspace",
            "sp24_orthogonalize", "sp24_orthogonalize_workspace", "sp24_muon_step", "sp24_muon_workspace",
-           "sp24_spmm_fwd_act", "sp24_spmm_bwd_input_act", "sp24_spmm_bwd_input_act_workspace",
+           "sp24_spmm_fwd_act", "sp24_spmm_fwd_act_workspace", "sp24_spmm_bwd_input_act", "sp24_spmm_bwd_input_act_workspace",
            "sp24_bias_grad", "sp24_bias_grad_workspace", "sp24_grad_norm", "sp24_grad_norm_workspace",
            "sp24_adamw_step", "sp24_state8_values",
            "sp24_status_str",
@@ -122,7 +122,8 @@ def lib() -> ctypes.CDLL:
             "sp24_orthogonalize_workspace": [p, i32],
             "sp24_muon_step": [p, i32, ctypes.c_float, i32, i32, p, i32, ctypes.c_float, p, i64, p],
             "sp24_muon_workspace": [p, i32],
-            "sp24_spmm_fwd_act": [p, p, p, i64, i64, i64, p, i32, p, p, p, p],
+            "sp24_spmm_fwd_act": [p, p, p, i64, i64, i64, p, i32, p, p, p, p, i64, p],
+            "sp24_spmm_fwd_act_workspace": [i64, i64, i64],
             "sp24_spmm_bwd_input_act": [p, p, p, i64, i64, i64, i32, p, p, p, p, i64, p],
             "sp24_spmm_bwd_input_act_workspace": [i64, i64, i64],
             "sp24_bias_grad": [p, i64, i64, p, p, i64, p],
@@ -658,7 +659,8 @@ def _addresses(*tensors):
     return res
 
 
-def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residual=None, U=False, out=None, stream=None):
+def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residual=None, U=False, out=None,
+                      workspace=None, stream=None):
     """Y [T, R] = act(U) + residual, U = X * Ws^T + bias (float32 [R]); each
     rounded once to float16.  U=True also returns U (a tensor may be passed
     instead); returns (Y, U or None).  ``out`` may be the residual."""
@@ -671,11 +673,16 @@ def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residu
         _need(bias, (R,), torch.float32, "bias")
     if residual is not None and (residual.dtype != f16 or residual.shape != (T, R)):
         _need(residual, (T, R), f16, "residual")
+    L = lib()
     with _using(stream):
         out = _out(out, (T, R), f16, X.device)
         U = None if U is False or U is None else _out(None if U is True else U, (T, R), f16, X.device)
-    x, v, m, b, r, u, y = _addresses(X, vals_row, meta_row, bias, residual, U, out)
-    _check("sp24_spmm_fwd_act", lib().sp24_spmm_fwd_act(x, v, m, T, R, C, b, kind, r, u, y, _stream(stream)))
+        need = L.sp24_spmm_fwd_act_workspace(T, R, C)
+        workspace = _workspace(workspace, need, X.device) if need else None
+    x, v, m, b, r, u, y, w = _addresses(X, vals_row, meta_row, bias, residual, U, out, workspace)
+    _check("sp24_spmm_fwd_act", L.sp24_spmm_fwd_act(
+        x, v, m, T, R, C, b, kind, r, u, y, w, 0 if w is None else workspace.numel() * workspace.element_size(),
+        _stream(stream)))
     return out, U
 
 
@@ -692,14 +699,12 @@ def sp24_spmm_bwd_input_act(dY, vals_col, meta_col, R, C, U, act="none", dbias=T
     _row_form(vals_col, meta_col, C, R, "the column form")
     if U is not None or kind:
         _need(U, (T, C), f16, "U")
-    L, need = lib(), 0
+    L = lib()
     with _using(stream):
         out = _out(out, (T, C), f16, dY.device)
-        if dbias is False or dbias is None:
-            dbias = None
-        else:
-            dbias = _out(None if dbias is True else dbias, (C,), torch.float32, dY.device)
-            need = L.sp24_spmm_bwd_input_act_workspace(T, R, C)
+        dbias = None if dbias is False or dbias is None else _out(None if dbias is True else dbias, (C,), torch.float32,
+                                                                  dY.device)
+        need = L.sp24_spmm_bwd_input_act_workspace(T, R, C)
         workspace = _workspace(workspace, need, dY.device) if need else None
     y, v, m, u, o, b, w = _addresses(dY, vals_col, meta_col, U, out, dbias, workspace)
     _check("sp24_spmm_bwd_input_act", L.sp24_spmm_bwd_input_act(

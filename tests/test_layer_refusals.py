@@ -24,19 +24,23 @@ def sp():
 
 
 def test_fwd_act(sp):
-    f = sp.lib().sp24_spmm_fwd_act
+    f, size = sp.lib().sp24_spmm_fwd_act, sp.lib().sp24_spmm_fwd_act_workspace
+    need = size(100, 32, 8192)
+    assert need > 0 and size(0, 32, 64) == 0 and size(1, 32, 64) == 0
+    assert size(-1, 32, 64) == -1 and size(4, 24, 64) == -1 and size(4, 2 ** 27, 64) == -1 and size(2 ** 31, 32, 64) == -1
 
-    def call(X=A, vals=A, meta=A, T=4, R=32, C=64, bias=A, act=3, residual=A, U=A, Y=A):
-        return f(X, vals, meta, T, R, C, bias, act, residual, U, Y, None)
+    def call(X=A, vals=A, meta=A, T=100, R=32, C=8192, bias=A, act=3, residual=A, U=A, Y=A, ws=A, n=need):
+        return f(X, vals, meta, T, R, C, bias, act, residual, U, Y, ws, n, None)
 
     assert call(act=-1) == UNSUPPORTED and call(act=6) == UNSUPPORTED
     assert call(T=-1) == SHAPE and call(R=24) == SHAPE and call(C=72) == SHAPE and call(R=-16) == SHAPE
     assert call(T=2 ** 31) == TOO_LARGE and call(R=2 ** 27) == TOO_LARGE and call(T=2 ** 30, C=2 ** 10) == TOO_LARGE
-    for k in ("X", "vals", "meta", "Y"):
+    for k in ("X", "vals", "meta", "Y", "ws"):
         assert call(**{k: None}) == NULL
-    for k in ("X", "vals", "meta", "Y", "bias", "residual", "U"):
+    for k in ("X", "vals", "meta", "Y", "bias", "residual", "U", "ws"):
         assert call(**{k: MIS}) == ALIGN
-    assert call(T=0, X=None, Y=None, bias=MIS) == OK and call(R=0, C=64, Y=None) == OK
+    assert call(n=need - 1) == WORKSPACE
+    assert call(T=0, X=None, Y=None, bias=MIS, ws=None) == OK and call(R=0, Y=None, ws=None) == OK
 
 
 def test_bwd_input_act(sp):

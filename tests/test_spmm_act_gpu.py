@@ -122,7 +122,8 @@ def test_forward(sp, act, T, R, C):
 
 @pytest.mark.parametrize("T,R,C", [(1, 1600, 6400), (1, 6400, 1600), (17, 1600, 6400), (24, 80, 4096), (32, 6400, 1600),
                                    (64, 112, 6400), (65, 1024, 320), (127, 64, 1616), (129, 336, 64), (257, 272, 128),
-                                   (300, 6400, 192), (1000, 128, 48), (1021, 1024, 4096), (2500, 528, 656)])
+                                   (300, 6400, 192), (1000, 128, 48), (1021, 1024, 4096), (2500, 528, 656),
+                                   (8192, 2064, 336)])
 def test_forward_sizes(sp, T, R, C):
     check_fwd(sp, T, R, C, "gelu", True, False, T % 2 == 0, seed=T)
 
@@ -142,7 +143,8 @@ def test_backward(sp, act, T, R, C):
 
 
 @pytest.mark.parametrize("T,R,C", [(1, 1600, 6400), (19, 1616, 6400), (64, 64, 1600), (65, 320, 1024), (129, 64, 336),
-                                   (257, 128, 272), (1021, 1024, 4096), (1000, 48, 128), (2500, 656, 528)])
+                                   (257, 128, 272), (1021, 1024, 4096), (1000, 48, 128), (2500, 656, 528), (24, 6416, 528), (150, 6400, 80),
+                                   (8100, 336, 2064)])
 def test_backward_sizes(sp, T, R, C):
     check_bwd(sp, T, R, C, "gelu", seed=T)
     check_bwd(sp, T, R, C, "relu", sums=False, seed=T)
@@ -244,16 +246,36 @@ def test_no_tokens_and_no_width(sp):
     assert torch.equal(Y, (bias + 1).half().expand(3, 32))
 
 
-@pytest.mark.parametrize("T", [9, 700])
-def test_in_place(sp, T):
-    f, _, gen = weight(sp, 320, 256, 3)
-    X, dY, res, U = (torch.randn(T, n, generator=gen, device="cuda").half() for n in (256, 320, 320, 256))
-    want, _ = sp.sp24_spmm_fwd_act(X, f["vals_row"], f["meta_row"], 320, 256, act="relu", residual=res)
-    got, _ = sp.sp24_spmm_fwd_act(X, f["vals_row"], f["meta_row"], 320, 256, act="relu", residual=res, out=res)
+@pytest.mark.parametrize("T,R,C", [(9, 320, 256), (700, 320, 256), (40, 1024, 1024)])
+def test_in_place(sp, T, R, C):
+    f, _, gen = weight(sp, R, C, 3)
+    X, dY, res, U = (torch.randn(T, n, generator=gen, device="cuda").half() for n in (C, R, R, C))
+    want, _ = sp.sp24_spmm_fwd_act(X, f["vals_row"], f["meta_row"], R, C, act="relu", residual=res)
+    got, _ = sp.sp24_spmm_fwd_act(X, f["vals_row"], f["meta_row"], R, C, act="relu", residual=res, out=res)
     assert torch.equal(got, want)
-    want, wb = sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], 320, 256, U, act="silu")
-    got, gb = sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], 320, 256, U, act="silu", out=U)
+    want, wb = sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], R, C, U, act="silu")
+    got, gb = sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], R, C, U, act="silu", out=U)
     assert torch.equal(got, want) and torch.equal(gb, wb)
+
+
+def test_workspace(sp):
+    """A call writes nothing past the workspace that it asked for."""
+    T, R, C = 150, 528, 6416
+    f, _, gen = weight(sp, R, C, 6)
+    X, dY, U = (torch.randn(T, n, generator=gen, device="cuda").half() for n in (C, R, C))
+    for need, call in (
+            (sp.lib().sp24_spmm_fwd_act_workspace(T, R, C),
+             lambda w: sp.sp24_spmm_fwd_act(X, f["vals_row"], f["meta_row"], R, C, act="gelu", workspace=w)),
+            (sp.lib().sp24_spmm_bwd_input_act_workspace(T, R, C),
+             lambda w: sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], R, C, U, act="gelu", workspace=w)),
+            (sp.lib().sp24_bias_grad_workspace(T, R), lambda w: (sp.sp24_bias_grad(dY, workspace=w),))):
+        assert need > 0
+        ws = Guarded((need,), torch.uint8)
+        got = call(ws.t)
+        ws.check("workspace")
+        assert all(a is None or torch.equal(a, b) for a, b in zip(got, call(None)))
+        with pytest.raises(ValueError):
+            call(ws.t[:need - 16])
 
 
 @pytest.mark.parametrize("T,R", [(1, 16), (1, 6400), (63, 48), (64, 512), (65, 528), (517, 1600), (4096, 1024),
