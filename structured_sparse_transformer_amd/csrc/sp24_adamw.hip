@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "sp24.h"
 #include "sp24_device.hpp"
@@ -95,12 +96,15 @@ __global__ __launch_bounds__(kThreads) void squares_kernel(NormTable tab, double
   const int k = tensor_of(tab.first, tab.count, blockIdx.x);
   const int64_t n = tab.n[k], i0 = (int64_t)(blockIdx.x - tab.first[k]) * kNormChunk;
   double sum = 0.0;
-  for (int u = 0; u < kNormChunk / (4 * kThreads); ++u) {
-    const int64_t i = i0 + (u * kThreads + (int)threadIdx.x) * 4;
-    if (i >= n) break;
-    const float4v x = load4<kF16>(tab.g[k], i, n);
+  constexpr int kAhead = 8;   // loads under way at once
+  for (int u0 = 0; u0 < kNormChunk / (4 * kThreads) && i0 + u0 * 4 * kThreads < n; u0 += kAhead) {
+    float4v x[kAhead];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)x[e], (double)x[e], sum);
+    for (int u = 0; u < kAhead; ++u) x[u] = load4<kF16>(tab.g[k], i0 + ((u0 + u) * kThreads + (int)threadIdx.x) * 4, n);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = __builtin_fma((double)x[u][e], (double)x[u][e], sum);
   }
   sum = wave_sum(sum);
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
@@ -181,6 +185,36 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// The largest of a row of 16 lanes, in all of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  const auto moved = [](uint32_t v, auto ctrl) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF, true);
+  };
+  x = max(x, moved(x, std::integral_constant<int, 0xB1>()));    // quad_perm 1 0 3 2
+  x = max(x, moved(x, std::integral_constant<int, 0x4E>()));    // quad_perm 2 3 0 1
+  x = max(x, moved(x, std::integral_constant<int, 0x124>()));   // row_ror 4
+  return max(x, moved(x, std::integral_constant<int, 0x128>()));   // row_ror 8
+}
+
+// Four codes, zeros past the end.
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
+  uint32_t c = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) c |= (uint32_t)p[i + e] << (8 * e);
+  return c;
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, uint32_t c) {
+  if (i + 4 <= n) {
+    *reinterpret_cast<uint32_t*>(p + i) = c;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) p[i + e] = (uint8_t)(c >> (8 * e));
+}
+
 // ---------------------------------------------------------------------------
 // AdamW.
 
@@ -225,128 +259,140 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable tab) {
   const float rate = t.lr / -expm1f((float)step * tab.ln_b1);
   const float root = 1.0f / sqrtf(-expm1f((float)step * tab.ln_b2));
   const uint32_t key = mix(mix(mix((uint32_t)step) ^ tab.seed) ^ t.place);
-  for (int u = 0; u < kAdamChunk / (4 * kThreads); ++u) {
-    const int64_t i = i0 + (u * kThreads + (int)threadIdx.x) * 4;
-    if (i0 + u * kThreads * 4 >= n) break;   // the whole workgroup: groups of lanes exchange values below
-    const float4v g = load4<kF16>(t.G, i, n);
-    float4v p = load4<false>(t.P, i, n), m, v, r;
-    if constexpr (k8) {
-      const bool in = i < n;
-      const int64_t j = in ? i : 0;
-      uint32_t mc = 0, vc = 0;
-      if (i + 4 <= n) {
-        mc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.M) + i);
-        vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.V) + i);
+  // groups of 4 entries, kAhead of them under way at once
+  constexpr int kGroups = kAdamChunk / (4 * kThreads), kAhead = k8 ? 4 : 2;
+  static_assert(kGroups % kAhead == 0, "whole batches");
+  for (int u0 = 0; u0 < kGroups && i0 + u0 * 4 * kThreads < n; u0 += kAhead) {
+    float4v g[kAhead], p[kAhead], m[kAhead], v[kAhead];
+    uint32_t mc[kAhead], vc[kAhead];
+    int me[kAhead], ve[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t i = i0 + ((u0 + u) * kThreads + (int)threadIdx.x) * 4;
+      g[u] = load4<kF16>(t.G, i, n);
+      p[u] = load4<false>(t.P, i, n);
+      if constexpr (k8) {
+        mc[u] = load_codes(static_cast<const uint8_t*>(t.M), i, n);
+        vc[u] = load_codes(static_cast<const uint8_t*>(t.V), i, n);
+        const int64_t group = (i < n ? i : 0) / 64;
+        me[u] = t.ME[group];
+        ve[u] = t.VE[group];
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < n) {
-            mc |= (uint32_t)static_cast<const uint8_t*>(t.M)[i + e] << (8 * e);
-            vc |= (uint32_t)static_cast<const uint8_t*>(t.V)[i + e] << (8 * e);
-          }
+        m[u] = load4<false>(t.M, i, n);
+        v[u] = load4<false>(t.V, i, n);
       }
-      const int me = t.ME[j / 64], ve = t.VE[j / 64];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = mc >> (8 * e) & 255, b = vc >> (8 * e) & 255;
-        const float x = held_value<kFracM>(a & 127, me);
-        m[e] = a & 128 ? -x : x;
-        r[e] = held_value<kFracV>(b, ve);
-        v[e] = r[e] * r[e];
-      }
-    } else {
-      m = load4<false>(t.M, i, n);
-      v = load4<false>(t.V, i, n);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = g[e] * factor;
-      m[e] = m[e] * tab.b1 + x * tab.c1;
-      v[e] = v[e] * tab.b2 + x * x * tab.c2;
-      r[e] = sqrtf(v[e]);
-      p[e] = p[e] * t.keep - rate * m[e] / (r[e] * root + tab.eps);
-    }
-    store4(t.P, i, n, p);
-    if (t.W != nullptr) {
-      if (i + 4 <= n) {
-        *reinterpret_cast<half4*>(t.W + i) = half4{(_Float16)p[0], (_Float16)p[1], (_Float16)p[2], (_Float16)p[3]};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < n) t.W[i + e] = __builtin_bit_cast(uint16_t, (_Float16)p[e]);
-      }
-    }
-    if constexpr (k8) {
-      // 16 lanes hold a group.  Lanes past the end hold zeros.
-      uint32_t tm = 0, tv = 0;
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t i = i0 + ((u0 + u) * kThreads + (int)threadIdx.x) * 4;
+      float r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (i + e >= n) m[e] = r[e] = 0.0f;
-        tm = max(tm, magnitude_bits(m[e]));
-        tv = max(tv, magnitude_bits(r[e]));
+        if constexpr (k8) {
+          const uint32_t a = mc[u] >> (8 * e) & 255, b = vc[u] >> (8 * e) & 255;
+          const float x = held_value<kFracM>(a & 127, me[u]), y = held_value<kFracV>(b, ve[u]);
+          m[u][e] = a & 128 ? -x : x;
+          v[u][e] = y * y;
+        }
+        const float x = g[u][e] * factor;
+        m[u][e] = m[u][e] * tab.b1 + x * tab.c1;
+        v[u][e] = v[u][e] * tab.b2 + x * x * tab.c2;
+        r[e] = sqrtf(v[u][e]);
+        p[u][e] = p[u][e] * t.keep - rate * m[u][e] / (r[e] * root + tab.eps);
       }
+      store4(t.P, i, n, p[u]);
+      if (t.W != nullptr) {
+        if (i + 4 <= n) {
+          *reinterpret_cast<half4*>(t.W + i) =
+              half4{(_Float16)p[u][0], (_Float16)p[u][1], (_Float16)p[u][2], (_Float16)p[u][3]};
+        } else {
 #pragma unroll
-      for (int x = 1; x < 16; x *= 2) {
-        tm = max(tm, (uint32_t)__shfl_xor((int)tm, x));
-        tv = max(tv, (uint32_t)__shfl_xor((int)tv, x));
+          for (int e = 0; e < 4; ++e)
+            if (i + e < n) t.W[i + e] = __builtin_bit_cast(uint16_t, (_Float16)p[u][e]);
+        }
       }
-      const int me = group_exponent<kFracM>(tm), ve = group_exponent<kFracV>(tv);
-      uint32_t mc = 0, vc = 0;
+      if constexpr (k8) {
+        // 16 lanes hold a group.  Entries past the end are zeros: the loads
+        // gave zeros, and a state of zeros stays one.
+        uint32_t tm = 0, tv = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t h = mix((uint32_t)(i + e) ^ key);
-        uint32_t a = me == 255 ? 0 : held_code<kFracM>(__builtin_fabsf(m[e]), me, h & 0xFFFFu);
-        uint32_t b = ve == 255 ? 0 : held_code<kFracV>(r[e], ve, h >> 16);
-        if (m[e] < 0.0f) a |= 128;
-        if (r[e] > 0.0f && b == 0) b = 1;
-        mc |= a << (8 * e);
-        vc |= b << (8 * e);
-      }
-      if (i + 4 <= n) {
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.M) + i) = mc;
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.V) + i) = vc;
+        for (int e = 0; e < 4; ++e) {
+          tm = max(tm, magnitude_bits(m[u][e]));
+          tv = max(tv, magnitude_bits(r[e]));
+        }
+        const int em = group_exponent<kFracM>(row_max(tm)), ev = group_exponent<kFracV>(row_max(tv));
+        uint32_t cm = 0, cv = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t bits = mix((uint32_t)(i + e) ^ key);
+          uint32_t a = held_code<kFracM>(__builtin_fabsf(m[u][e]), em, bits & 0xFFFFu);
+          uint32_t b = held_code<kFracV>(r[e], ev, bits >> 16);
+          if (m[u][e] < 0.0f) a |= 128;
+          if (r[e] > 0.0f) b = max(b, 1u);
+          cm |= a << (8 * e);
+          cv |= b << (8 * e);
+        }
+        store_codes(static_cast<uint8_t*>(t.M), i, n, em == 255 ? 0 : cm);
+        store_codes(static_cast<uint8_t*>(t.V), i, n, ev == 255 ? 0 : cv);
+        if ((threadIdx.x & 15) == 0 && i < n) {
+          t.ME[i / 64] = (uint8_t)em;
+          t.VE[i / 64] = (uint8_t)ev;
+        }
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < n) {
-            static_cast<uint8_t*>(t.M)[i + e] = (uint8_t)(mc >> (8 * e));
-            static_cast<uint8_t*>(t.V)[i + e] = (uint8_t)(vc >> (8 * e));
-          }
+        store4(static_cast<float*>(t.M), i, n, m[u]);
+        store4(static_cast<float*>(t.V), i, n, v[u]);
       }
-      if ((threadIdx.x & 15) == 0 && i < n) {
-        t.ME[i / 64] = (uint8_t)me;
-        t.VE[i / 64] = (uint8_t)ve;
-      }
-    } else {
-      store4(static_cast<float*>(t.M), i, n, m);
-      store4(static_cast<float*>(t.V), i, n, v);
     }
   }
 }
 
-// What a state of 8 bits stands for.
+// What a state of 8 bits stands for, 16 entries a lane.
 template <bool kRoot, bool kBf16>
 __global__ __launch_bounds__(kThreads) void state8_values_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint8_t* __restrict__ exps, int64_t n,
                                                                  void* __restrict__ out) {
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16;
   if (i >= n) return;
   const int E = exps[i / 64];
-  float x[4];
+  uint32_t c[4];
+  if (i + 16 <= n) {
+    const uint4 all = *reinterpret_cast<const uint4*>(codes + i);
+    c[0] = all.x;
+    c[1] = all.y;
+    c[2] = all.z;
+    c[3] = all.w;
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t c = i + e < n ? codes[i + e] : 0;
-    x[e] = kRoot ? held_value<kFracV>(c, E) : held_value<kFracM>(c & 127, E);
-    if (!kRoot && c & 128) x[e] = -x[e];
+    for (int k = 0; k < 4; ++k) c[k] = load_codes(codes, i + 4 * k, n);
+  }
+  float x[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint32_t a = c[e / 4] >> (8 * (e % 4)) & 255;
+    x[e] = kRoot ? held_value<kFracV>(a, E) : held_value<kFracM>(a & 127, E);
+    if (!kRoot && a & 128) x[e] = -x[e];
   }
   if constexpr (kBf16) {
     // five significant bits at most: the upper half holds them all
-    uint16_t* o = static_cast<uint16_t*>(out) + i;
+    uint16_t* const o = static_cast<uint16_t*>(out) + i;
+    const auto upper = [&](int e) { return __builtin_bit_cast(uint32_t, x[e]) >> 16; };
+    if (i + 16 <= n) {
+      uint4 w[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < n) o[e] = (uint16_t)(__builtin_bit_cast(uint32_t, x[e]) >> 16);
+      for (int k = 0; k < 2; ++k)
+        w[k] = make_uint4(upper(8 * k) | upper(8 * k + 1) << 16, upper(8 * k + 2) | upper(8 * k + 3) << 16,
+                          upper(8 * k + 4) | upper(8 * k + 5) << 16, upper(8 * k + 6) | upper(8 * k + 7) << 16);
+      reinterpret_cast<uint4*>(o)[0] = w[0];
+      reinterpret_cast<uint4*>(o)[1] = w[1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (i + e < n) o[e] = (uint16_t)upper(e);
+    }
   } else {
-    store4(static_cast<float*>(out), i, n, float4v{x[0], x[1], x[2], x[3]});
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      store4(static_cast<float*>(out), i + 4 * k, n, float4v{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]});
   }
 }
 
@@ -439,7 +485,7 @@ hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, boo
 hipError_t launch_state8_values(const uint8_t* codes, const uint8_t* exps, int64_t n, bool root, bool bf16, void* out,
                                 hipStream_t s) {
   if (n == 0) return hipSuccess;
-  const dim3 grid((unsigned)chunks_of(n, 4 * kThreads)), block(kThreads);
+  const dim3 grid((unsigned)chunks_of(n, 16 * kThreads)), block(kThreads);
   if (root && bf16) hipLaunchKernelGGL((state8_values_kernel<true, true>), grid, block, 0, s, codes, exps, n, out);
   else if (root) hipLaunchKernelGGL((state8_values_kernel<true, false>), grid, block, 0, s, codes, exps, n, out);
   else if (bf16) hipLaunchKernelGGL((state8_values_kernel<false, true>), grid, block, 0, s, codes, exps, n, out);

@@ -16,10 +16,12 @@ of such a tensor is not a row of the form.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -675,7 +677,7 @@ def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residu
         _need(residual, (T, R), f16, "residual")
     L = lib()
     with _using(stream):
-        out = _out(out, (T, R), f16, X.device)
+        out = X.new_empty((T, R)) if out is None else _out(out, (T, R), f16, X.device)
         U = None if U is False or U is None else _out(None if U is True else U, (T, R), f16, X.device)
         need = L.sp24_spmm_fwd_act_workspace(T, R, C)
         workspace = _workspace(workspace, need, X.device) if need else None
@@ -745,23 +747,27 @@ def _control(control):
     return _need(control, (8,), torch.int32, "the control")
 
 
-def _pointers(tensors, dtype, name):
-    """Addresses of many tensors; _ptr's checks, each once over all of them."""
-    if any(t.dtype != dtype for t in tensors):
-        raise ValueError(f"{name} must be {dtype}")
-    if not all([t.is_contiguous() for t in tensors]):
-        raise ValueError(f"{name} must be contiguous")
-    device = torch.cuda.current_device() if tensors else 0
-    if any([t.get_device() != device for t in tensors]):   # -1 for host memory
-        raise ValueError(f"{name} must be on the current device, cuda:{device}")
-    return [t.data_ptr() for t in tensors]
+def _gradients(grads):
+    """Checks many gradients, each of _ptr's checks over all of them at once, and
+    gives their type's number, addresses and sizes."""
+    Tensor, types = torch.Tensor, {t.dtype for t in grads}
+    if not types:
+        return F32, [], []
+    kind = {torch.float16: F16, torch.float32: F32}.get(types.pop())
+    if kind is None or types:
+        raise ValueError("gradients must be all float16 or all float32")
+    if not all(map(Tensor.is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous")
+    devices = set(map(Tensor.get_device, grads))
+    if -1 in devices or devices != {torch.cuda.current_device()}:   # -1: host memory
+        raise ValueError("gradients must be on the current device")
+    return kind, list(map(Tensor.data_ptr, grads)), list(map(Tensor.numel, grads))
 
 
-def _grad_type(grads):
-    types = {torch.float16: F16, torch.float32: F32}
-    if grads and grads[0].dtype not in types:
-        raise ValueError("gradients must be float16 or float32")
-    return (grads[0].dtype, types[grads[0].dtype]) if grads else (torch.float32, F32)
+def _int64s(values):
+    """An array of 64-bit numbers that the library reads, and its address."""
+    a = array.array("q", values)
+    return a, a.buffer_info()[0] or None
 
 
 def sp24_grad_norm(grads, scale=1.0, max_norm=float("inf"), control=None, workspace=None, stream=None):
@@ -769,19 +775,17 @@ def sp24_grad_norm(grads, scale=1.0, max_norm=float("inf"), control=None, worksp
     shapes) times ``scale``, and the factor that takes the scale off them and
     clips them to ``max_norm``, in a control (see step_control; one is made
     unless given), whose step grows by 1 unless some gradient is not finite."""
-    dtype, kind = _grad_type(grads)
-    n = len(grads)
-    pointers = (ctypes.c_void_p * n)(*_pointers(grads, dtype, "gradients"))
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    sizes_p = ctypes.cast(sizes, ctypes.c_void_p)
+    kind, pointers, sizes = _gradients(grads)
+    n, L = len(grads), lib()
+    (pointers, at), (sizes, sizes_at) = _int64s(pointers), _int64s(sizes)
     with _using(stream):
         if control is None:
             control = step_control(torch.device("cuda", torch.cuda.current_device()))
         _control(control)
-        workspace = _workspace(workspace, lib().sp24_grad_norm_workspace(sizes_p, n), control.device)
-    _check("sp24_grad_norm", lib().sp24_grad_norm(
-        ctypes.cast(pointers, ctypes.c_void_p), sizes_p, n, kind, float(scale), float(max_norm), _ptr(control),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace = _workspace(workspace, L.sp24_grad_norm_workspace(sizes_at, n), control.device)
+    c, w = _addresses(control, workspace)
+    _check("sp24_grad_norm", L.sp24_grad_norm(
+        at, sizes_at, n, kind, float(scale), float(max_norm), c, w, workspace.numel() * workspace.element_size(), _stream(stream)))
     return control
 
 
@@ -791,6 +795,10 @@ class AdamwPlan:
 
     def __init__(self, jobs, tensors, sizes, state8):
         self.jobs, self.tensors, self.sizes, self.state8 = jobs, tensors, sizes, state8
+        self.address = ctypes.addressof(jobs) if sizes else None
+        # the jobs' first fields, the gradients' addresses
+        words = np.frombuffer(jobs, dtype=np.int64) if sizes else np.zeros(0, dtype=np.int64)
+        self.gradients = words[::ctypes.sizeof(AdamwJob) // 8]
 
 
 def sp24_adamw_plan(Ps, Ms, Vs, Ws=None, lrs=1e-3, decays=0.0, M_exps=None, V_exps=None):
@@ -832,17 +840,16 @@ def sp24_adamw_step(plan, Gs, betas=(0.9, 0.999), eps=1e-8, step=None, control=N
     that sp24_grad_norm wrote says."""
     if (step is None) == (control is None):
         raise ValueError("either step or control")
-    if len(Gs) != len(plan.sizes) or [G.numel() for G in Gs] != plan.sizes:
+    kind, pointers, sizes = _gradients(Gs)
+    if sizes != plan.sizes:
         raise ValueError("one gradient per tensor, of its size")
-    dtype, kind = _grad_type(Gs)
-    for job, pointer in zip(plan.jobs, _pointers(Gs, dtype, "gradients")):
-        job.G = pointer
-    if plan.tensors[0] and plan.tensors[0][0].get_device() != torch.cuda.current_device():
+    if pointers and plan.tensors[0][0].get_device() != Gs[0].get_device():
         raise ValueError("the plan's tensors are not on the current device")
+    plan.gradients[:] = pointers
+    control = None if control is None else _addresses(_control(control))[0]
     _check("sp24_adamw_step", lib().sp24_adamw_step(
-        ctypes.cast(plan.jobs, ctypes.c_void_p), len(plan.sizes), kind, STATE8 if plan.state8 else F32, float(betas[0]),
-        float(betas[1]), float(eps), 0 if step is None else int(step),
-        None if control is None else _ptr(_control(control)), int(seed) & 0xFFFFFFFF, _stream(stream)))
+        plan.address, len(sizes), kind, STATE8 if plan.state8 else F32, float(betas[0]), float(betas[1]), float(eps),
+        0 if step is None else int(step), control, int(seed) & 0xFFFFFFFF, _stream(stream)))
 
 
 def state8(P):
