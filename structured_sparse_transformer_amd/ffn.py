@@ -19,6 +19,14 @@ and its backward
     dX  = dU W1s,   dW1 = dU^T X  + decay (1 - M1) W1
 
 with W1 [2h, d] and W2 [d, h] the dense fp16 master weights, Ms their masks.
+SparseFFN is the plain layer, with biases, an activation and a residual:
+
+    U  = X W1s^T + b1,  H = act(U)        [T, h]   (one product)
+    Y  = H W2s^T + b2 + X                 [T, d]   (one product)
+
+    dU = (dY W2s) act'(U),  db1 = sum dU  (one product)
+    db2 = sum dY,  dW2 = dY^T H + decay (1 - M2) W2
+    dX = dU W1s + dY,       dW1 = dU^T X + decay (1 - M1) W1
 """
 from __future__ import annotations
 
@@ -38,16 +46,11 @@ class Saved:
     Hg: torch.Tensor
 
 
-class SparseGegluFFN:
-    """W1 fp16 [2h, d] in blocks of 16 value rows then 16 gate rows, W2 fp16
-    [d, h]; h a multiple of 16.  `refresh()` searches and compresses both
-    weights (and adds each weight's flipped mask entries to `flips` once
-    masks exist); `forward` and `backward` run the step."""
+class _TwoWeights:
+    """Two dense weights, their 2:4 forms and the streams that a backward pass
+    uses."""
 
-    def __init__(self, W1: torch.Tensor, W2: torch.Tensor, decay: float = 0.0):
-        two_h, d = W1.shape
-        if W2.shape != (d, two_h // 2) or two_h % 32 != 0:
-            raise ValueError("W1 must be [2h, d] with 2h a multiple of 32, W2 [d, h]")
+    def __init__(self, W1: torch.Tensor, W2: torch.Tensor, decay: float):
         self.W1, self.W2, self.decay = W1, W2, float(decay)
         self.forms = None
         self.flips = torch.zeros(2, dtype=torch.int64, device=W1.device)
@@ -66,6 +69,25 @@ class SparseGegluFFN:
             raise RuntimeError("call refresh() first: the layer has no compressed weights yet")
         return self.forms
 
+    def _streams(self):
+        main = torch.cuda.current_stream()
+        if self._side is None:
+            self._side = torch.cuda.Stream(device=main.device)
+        return main, self._side
+
+
+class SparseGegluFFN(_TwoWeights):
+    """W1 fp16 [2h, d] in blocks of 16 value rows then 16 gate rows, W2 fp16
+    [d, h]; h a multiple of 16.  `refresh()` searches and compresses both
+    weights (and adds each weight's flipped mask entries to `flips` once
+    masks exist); `forward` and `backward` run the step."""
+
+    def __init__(self, W1: torch.Tensor, W2: torch.Tensor, decay: float = 0.0):
+        two_h, d = W1.shape
+        if W2.shape != (d, two_h // 2) or two_h % 32 != 0:
+            raise ValueError("W1 must be [2h, d] with 2h a multiple of 32, W2 [d, h]")
+        super().__init__(W1, W2, decay)
+
     def forward(self, X: torch.Tensor):
         f1, f2 = self._current_forms()
         two_h, d = self.W1.shape
@@ -80,10 +102,7 @@ class SparseGegluFFN:
         every output is allocated on the caller's stream."""
         f1, f2 = self._current_forms()
         two_h, d = self.W1.shape
-        main = torch.cuda.current_stream()
-        if self._side is None:
-            self._side = torch.cuda.Stream(device=main.device)
-        side = self._side
+        main, side = self._streams()
         dW2 = torch.empty(d, two_h // 2, dtype=torch.float32, device=dY.device)
         dHg = sp24.sp24_spmm_bwd_input(dY, f2["vals_col"], f2["meta_col"], d, two_h // 2)
         side.wait_stream(main)
@@ -93,3 +112,54 @@ class SparseGegluFFN:
         dW1 = sp24.sp24_weight_grad(dU, saved.X, self.W1, f1["idx"], self.decay)
         main.wait_stream(side)
         return dX, dW1, dW2
+
+
+class SparseFFN(_TwoWeights):
+    """The plain layer: W1 fp16 [h, d], b1 fp32 [h], W2 fp16 [d, h], b2 fp32 [d],
+    both widths multiples of 16; ``act`` as sp24.ACTIVATIONS has it; ``residual``
+    adds the layer's input to its output."""
+
+    def __init__(self, W1: torch.Tensor, b1: torch.Tensor, W2: torch.Tensor, b2: torch.Tensor, act: str = "gelu",
+                 residual: bool = True, decay: float = 0.0):
+        h, d = W1.shape
+        if W2.shape != (d, h) or b1.shape != (h,) or b2.shape != (d,):
+            raise ValueError("W1 must be [h, d], b1 [h], W2 [d, h], b2 [d]")
+        if act not in sp24.ACTIVATIONS:
+            raise ValueError(f"act must be one of {', '.join(sp24.ACTIVATIONS)}")
+        super().__init__(W1, W2, decay)
+        self.b1, self.b2, self.act, self.residual = b1, b2, act, residual
+
+    def _products(self, X, keep):
+        f1, f2 = self._current_forms()
+        h, d = self.W1.shape
+        H, U = sp24.sp24_spmm_fwd_act(X, f1["vals_row"], f1["meta_row"], h, d, act=self.act, bias=self.b1, U=keep)
+        Y, _ = sp24.sp24_spmm_fwd_act(H, f2["vals_row"], f2["meta_row"], d, h, bias=self.b2,
+                                      residual=X if self.residual else None)
+        return Y, U, H
+
+    def __call__(self, X: torch.Tensor) -> torch.Tensor:
+        """The output alone, for one token as for many."""
+        return self._products(X, False)[0]
+
+    def forward(self, X: torch.Tensor):
+        Y, U, H = self._products(X, True)
+        return Y, Saved(X, U, H)
+
+    def backward(self, dY: torch.Tensor, saved: Saved):
+        """dX, dW1, db1, dW2, db2.  dW2 and db2 run on a second stream beside dU
+        and dX, as in SparseGegluFFN."""
+        f1, f2 = self._current_forms()
+        h, d = self.W1.shape
+        main, side = self._streams()
+        dW2 = torch.empty(d, h, dtype=torch.float32, device=dY.device)
+        db2 = torch.empty(d, dtype=torch.float32, device=dY.device)
+        work = torch.empty(sp24.lib().sp24_bias_grad_workspace(*dY.shape), dtype=torch.uint8, device=dY.device)
+        dU, db1 = sp24.sp24_spmm_bwd_input_act(dY, f2["vals_col"], f2["meta_col"], d, h, saved.U, act=self.act)
+        side.wait_stream(main)
+        sp24.sp24_weight_grad(dY, saved.Hg, self.W2, f2["idx"], self.decay, dW=dW2, stream=side)
+        sp24.sp24_bias_grad(dY, dbias=db2, workspace=work, stream=side)
+        # dU W1s + dY: the column form is the row form of the transpose
+        dX, _ = sp24.sp24_spmm_fwd_act(dU, f1["vals_col"], f1["meta_col"], d, h, residual=dY if self.residual else None)
+        dW1 = sp24.sp24_weight_grad(dU, saved.X, self.W1, f1["idx"], self.decay)
+        main.wait_stream(side)
+        return dX, dW1, db1, dW2, db2
