@@ -25,6 +25,8 @@ namespace {
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
+constexpr int64_t kCus = 256;   // of an MI355X
+
 // What a product's epilogue reads and writes besides the product.
 struct Finish {
   const float* bias;       // [N] or null (forward)
@@ -213,6 +215,12 @@ hipError_t launch_thin(const uint16_t* A, const uint16_t* vals, const uint16_t* 
 // the first half of its 512 bytes and the odd ones in the second, each half
 // XOR-swizzled by the token, so that 8 lanes that write one chunk of 8 tokens,
 // and 16 that read 16 chunks of one, meet no bank twice.
+//
+// Two workgroups share a CU, so that the matrix units have one's products while
+// the other is in its epilogue: a ring of two slots for 256 x 128 tiles.  (One
+// workgroup of 256 x 256 with three slots, at 16384 x 6400 x 1600: no epilogue
+// work 232 us, GELU 267, backward through GELU 310; two of 256 x 128: 226, 244 and
+// 284.)
 template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
 __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, const uint16_t* __restrict__ A,
                                               const uint16_t* __restrict__ vals, const uint16_t* __restrict__ meta,
@@ -357,43 +365,99 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
   }
 }
 
-template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), 2) void spmm_act_kernel(
-    const uint16_t* __restrict__ A, const uint16_t* __restrict__ vals, const uint16_t* __restrict__ meta, int64_t T,
-    int64_t N, int64_t K, Finish fin, int tiles_m, int tiles_n) {
-  using Cfg = FastCfg<BM, BN, WM, WN>;
-  __shared__ __align__(1024) unsigned char smem[kSlots * (Cfg::S_BYTES + Cfg::B_BYTES + Cfg::M_BYTES)];
-  static_assert(WM == 128 && WN % 32 == 0 && Cfg::WAVES * 16384 <= sizeof(smem), "staging");
-
-  // tile order as in the products alone: groups of 8 feature tiles, token tiles
-  // within a group, features fastest, a contiguous run of it for each XCD
+// Tile `lin` of tiles_m x tiles_n in the order of the products alone: groups of 8
+// feature tiles, token tiles within a group, features fastest.
+__device__ __forceinline__ void tile_at(int lin, int tiles_m, int tiles_n, int& tm, int& tn) {
   constexpr int kGroupM = 8;
-  const int ntiles = tiles_m * tiles_n, per_xcd = (ntiles + 7) / 8;
-  const int lin = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
-  if (lin >= ntiles) return;
   const int group = lin / (kGroupM * tiles_n), gm0 = group * kGroupM, gsize = min(kGroupM, tiles_m - gm0);
   const int in_group = lin - group * kGroupM * tiles_n;
-  const int tn = __builtin_amdgcn_readfirstlane(in_group / gsize);
-  const int tm = __builtin_amdgcn_readfirstlane(gm0 + in_group % gsize);
+  tn = __builtin_amdgcn_readfirstlane(in_group / gsize);
+  tm = __builtin_amdgcn_readfirstlane(gm0 + in_group % gsize);
+}
 
-  // the tile's tokens as a matrix of their own, so that the direct loads' 32-bit
-  // offsets count from its first row however many tokens there are
+// The tile's tokens are a matrix of their own to it, so that the direct loads'
+// 32-bit offsets count from its first row however many tokens there are.
+template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
+__device__ __forceinline__ void spmm_act_at(unsigned char* smem, const uint16_t* A, const uint16_t* vals,
+                                            const uint16_t* meta, int64_t T, int64_t N, int64_t K, const Finish& fin,
+                                            int tm, int tn) {
   const int64_t t0 = (int64_t)tn * BN;
   spmm_act_tile<BM, BN, WM, WN, kSlots, kBwd, kTail>(smem, A + t0 * K, vals, meta, T - t0 < BN ? T - t0 : BN, N, K, tm, 0,
                                                      (int)threadIdx.x, fin, t0);
 }
 
-template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd>
-hipError_t launch_tiles(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
+template <int BM, int BN>
+constexpr int tile_bytes(int slots) { return slots * (BM * 72 + BN * 128); }
+
+// 256 x 128 tiles of the first `big` x 256 features and 128 x 128 tiles of the
+// others, after them: the last, partly filled round of workgroups takes half as
+// long, and a strip of up to 128 features no more than its own work.  (16384 x
+// 6400 x 1600, 24 strips and two halves instead of 25: forward with GELU 268 -> 257 us, backward 284 -> 277.)  Each XCD
+// takes a contiguous run of either.
+template <bool kBwd, bool kTail>
+__global__ __launch_bounds__(256, 2) void spmm_large_kernel(const uint16_t* __restrict__ A,
+                                                            const uint16_t* __restrict__ vals,
+                                                            const uint16_t* __restrict__ meta, int64_t T, int64_t N,
+                                                            int64_t K, Finish fin, int big, int tiles_n) {
+  __shared__ __align__(1024) unsigned char smem[tile_bytes<256, 128>(2)];
+  static_assert(sizeof(smem) >= tile_bytes<128, 128>(2) && sizeof(smem) >= 4 * 16384, "either tile and its staging");
+  const int nbig = big * tiles_n, big_per_xcd = (nbig + 7) / 8;
+  const int x = (int)(blockIdx.x % 8), at = (int)(blockIdx.x / 8);
+  int tm, tn;
+  if (at < big_per_xcd) {
+    const int lin = x * big_per_xcd + at;
+    if (lin >= nbig) return;
+    tile_at(lin, big, tiles_n, tm, tn);
+    spmm_act_at<256, 128, 128, 64, 2, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, tm, tn);
+  } else {
+    const int small = (int)((N - big * 256 + 127) / 128), nsmall = small * tiles_n, per_xcd = (nsmall + 7) / 8;
+    const int lin = x * per_xcd + at - big_per_xcd;
+    if (at - big_per_xcd >= per_xcd || lin >= nsmall) return;
+    tile_at(lin, small, tiles_n, tm, tn);
+    spmm_act_at<128, 128, 128, 32, 2, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, 2 * big + tm, tn);
+  }
+}
+
+template <bool kBwd>
+hipError_t launch_large(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
                         const Finish& f, hipStream_t s) {
-  const int tiles_m = (int)((N + BM - 1) / BM), tiles_n = (int)((T + BN - 1) / BN);
-  const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8)), block(FastCfg<BM, BN, WM, WN>::THREADS);
+  const int64_t tiles_n = (T + 127) / 128, slots = 2 * kCus, rounds = tiles_n * ((N + 255) / 256) / slots;
+  // as many strips as fill whole rounds, if the rest takes one round of small tiles
+  int64_t big = std::min(N / 256, rounds * slots / tiles_n);
+  if ((N - big * 256 + 127) / 128 * tiles_n > slots) big = N / 256;
+  const int64_t small = (N - big * 256 + 127) / 128;
+  const dim3 grid((unsigned)(((big * tiles_n + 7) / 8 + (small * tiles_n + 7) / 8) * 8)), block(256);
   if (K % 64 == 0)
-    hipLaunchKernelGGL((spmm_act_kernel<BM, BN, WM, WN, kSlots, kBwd, false>), grid, block, 0, s, A, vals, meta, T, N, K, f,
-                       tiles_m, tiles_n);
+    hipLaunchKernelGGL((spmm_large_kernel<kBwd, false>), grid, block, 0, s, A, vals, meta, T, N, K, f, (int)big, (int)tiles_n);
   else
-    hipLaunchKernelGGL((spmm_act_kernel<BM, BN, WM, WN, kSlots, kBwd, true>), grid, block, 0, s, A, vals, meta, T, N, K, f,
-                       tiles_m, tiles_n);
+    hipLaunchKernelGGL((spmm_large_kernel<kBwd, true>), grid, block, 0, s, A, vals, meta, T, N, K, f, (int)big, (int)tiles_n);
+  return hipGetLastError();
+}
+
+// 128 x 128 tiles throughout, with a three-slot ring.
+template <bool kBwd, bool kTail>
+__global__ __launch_bounds__(256, 2) void spmm_small_kernel(const uint16_t* __restrict__ A,
+                                                            const uint16_t* __restrict__ vals,
+                                                            const uint16_t* __restrict__ meta, int64_t T, int64_t N,
+                                                            int64_t K, Finish fin, int tiles_m, int tiles_n) {
+  __shared__ __align__(1024) unsigned char smem[tile_bytes<128, 128>(3)];
+  const int ntiles = tiles_m * tiles_n, per_xcd = (ntiles + 7) / 8;
+  const int lin = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
+  if (lin >= ntiles) return;
+  int tm, tn;
+  tile_at(lin, tiles_m, tiles_n, tm, tn);
+  spmm_act_at<128, 128, 128, 32, 3, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, tm, tn);
+}
+
+template <bool kBwd>
+hipError_t launch_small(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
+                        const Finish& f, hipStream_t s) {
+  const int tiles_m = (int)((N + 127) / 128), tiles_n = (int)((T + 127) / 128);
+  const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8)), block(256);
+  if (K % 64 == 0)
+    hipLaunchKernelGGL((spmm_small_kernel<kBwd, false>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n);
+  else
+    hipLaunchKernelGGL((spmm_small_kernel<kBwd, true>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -627,7 +691,6 @@ struct Plan {
 };
 
 Plan plan_product(int64_t T, int64_t N, int64_t K) {
-  constexpr int64_t kCus = 256;   // of an MI355X
   const auto tiles = [&](int64_t features, int64_t tokens) {
     return ((T + tokens - 1) / tokens) * ((N + features - 1) / features);
   };
@@ -650,8 +713,8 @@ hipError_t launch_product(const Plan& p, const uint16_t* A, const uint16_t* vals
                           int64_t N, int64_t K, const Finish& fin, float* ws, hipStream_t s) {
   switch (p.how) {
     case Plan::kThin: return launch_thin<kBwd>(A, vals, meta, T, N, K, fin, s);
-    case Plan::kSmall: return launch_tiles<128, 128, 128, 32, 3, kBwd>(A, vals, meta, T, N, K, fin, s);
-    case Plan::kLarge: return launch_tiles<256, 128, 128, 64, 2, kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kSmall: return launch_small<kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kLarge: return launch_large<kBwd>(A, vals, meta, T, N, K, fin, s);
     case Plan::kMid: break;
   }
   if (p.parts == 1) return launch_mid<kBwd ? kBackward : kForward>(A, vals, meta, T, N, K, fin, 1, s);
