@@ -201,6 +201,10 @@ hipError_t launch_thin(const uint16_t* A, const uint16_t* vals, const uint16_t* 
   return hipSuccess;
 }
 
+// LDS of a tile's ring.
+template <int BM, int BN>
+constexpr int tile_bytes(int slots) { return slots * (BM * 72 + BN * 128); }
+
 // ---------------------------------------------------------------------------
 // Products of many tokens: the tile of sp24_spmm_tile.hpp.
 //
@@ -221,14 +225,28 @@ hipError_t launch_thin(const uint16_t* A, const uint16_t* vals, const uint16_t* 
 // workgroup of 256 x 256 with three slots, at 16384 x 6400 x 1600: no epilogue
 // work 232 us, GELU 267, backward through GELU 310; two of 256 x 128: 226, 244 and
 // 284.)
-template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
-__device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, const uint16_t* __restrict__ A,
+//
+// With kGroups = 2 a workgroup has two groups of waves, each of which sums up half
+// of the stages of the whole tile, through a ring of its own at smem + group *
+// kRing; their sums meet in the staging, and each finishes half of the tokens.
+template <int BM, int BN, int WM, int WN, int kSlots, int kGroups, bool kBwd, bool kTail>
+__device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ base, const uint16_t* __restrict__ A,
                                               const uint16_t* __restrict__ vals, const uint16_t* __restrict__ meta,
-                                              int64_t T, int64_t N, int64_t K, int tm, int tn, int tid,
+                                              int64_t T, int64_t N, int64_t K, int tm, int tn, int thread,
                                               const Finish& fin, int64_t t0) {
+  static_assert(kGroups == 1 || (kGroups == 2 && WN == 32), "a group finishes 16 of a wave's 32 tokens");
+  constexpr int kThreads = FastCfg<BM, BN, WM, WN>::THREADS, kWaves = kThreads / 64;
+  const int group = kGroups == 1 ? 0 : __builtin_amdgcn_readfirstlane(thread / kThreads);
+  const int tid = kGroups == 1 ? thread : thread % kThreads;
+  unsigned char* const smem = base + group * tile_bytes<BM, BN>(kSlots);
+  const int n = (int)(K / 64), half = (n + kGroups - 1) / kGroups, kt0 = group * half;
+  const auto stages = [&] { return kGroups == 1 ? n : group == 0 ? half : n - half; };
 #include "sp24_spmm_loop.inc"
+  // the second of an odd number of stages' halves has one stage less: its waves
+  // meet the others' last barrier here
+  if (kGroups == 2 && n % 2 != 0 && group == 1) __builtin_amdgcn_s_barrier();
 
-  if constexpr (kTail) {
+  if (kTail && group == kGroups - 1) {
     // the last 16, 32 or 48 of the reduction, a narrower block of the forms:
     // straight from memory, zeros past its end
     const int64_t k0 = K / 64 * 64;
@@ -266,7 +284,7 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();   // no wave reads the ring any more
   asm volatile("" ::: "memory");
-  unsigned char* const staged = smem + (size_t)wave * 16384;
+  unsigned char* const staged = base + (size_t)(group * kWaves + wave) * 16384;
   const int q = lane & 15;        // this lane's 8 features
   const int64_t m = m0 + wm * WM + 8 * q;
   const bool inside = m < N;
@@ -279,15 +297,16 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
   // (Four: 293 us with a residual at 16384 x 6400 x 1600, eight: 276; none
   // early: 304.)
   const uint16_t* const beside = kBwd ? fin.u_in : fin.add;
-  h8 next[8];
-  const int first = lane >> 4, last = (int)T - 1;
+  constexpr int kPasses = 8 / kGroups;
+  h8 next[kPasses];
+  const int first = group * (4 * kPasses) + (lane >> 4), last = (int)T - 1;
   const uint16_t* const from_m = beside + t0 * N + (inside ? m : 0);
   const auto fetch = [&](int pass) {
     return *reinterpret_cast<const h8*>(from_m + (int64_t)min(wn * WN + pass * 4 + first, last) * N);
   };
   if (beside != nullptr)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) next[k] = fetch(k);
+    for (int k = 0; k < kPasses; ++k) next[k] = fetch(k);
   float sums[8] = {};
 #pragma unroll
   for (int nt = 0; nt < Cfg::TN; ++nt) {
@@ -299,15 +318,20 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
         *reinterpret_cast<float4v*>(staged + l32 * 512 + g * 256 + (((mt * 4 + i4) ^ (l32 & 15)) * 16)) =
             float4v{a[4 * i4], a[4 * i4 + 1], a[4 * i4 + 2], a[4 * i4 + 3]};
       }
-    // the wave reads back only what it wrote, in order: no barrier is needed
+    // of one group, the wave reads back only what it wrote, in order: no barrier is needed
+    if constexpr (kGroups == 2) __syncthreads();
     with_act(fin.act, [&](auto kind) __attribute__((always_inline)) {
       constexpr int kAct = decltype(kind)::value;
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
+      for (int it = 0; it < kPasses; ++it) {
         const int t = it * 4 + first;
-        const unsigned char* const from = staged + t * 512 + ((q ^ (t & 15)) * 16);
-        const float4v lo = *reinterpret_cast<const float4v*>(from);
-        const float4v hi = *reinterpret_cast<const float4v*>(from + 256);
+        const unsigned char* const from = base + wave * 16384 + t * 512 + ((q ^ (t & 15)) * 16);
+        float4v lo = *reinterpret_cast<const float4v*>(from);
+        float4v hi = *reinterpret_cast<const float4v*>(from + 256);
+        if constexpr (kGroups == 2) {
+          lo += *reinterpret_cast<const float4v*>(from + kWaves * 16384);
+          hi += *reinterpret_cast<const float4v*>(from + kWaves * 16384 + 256);
+        }
         const h8 now = next[it];
         if (beside != nullptr && nt + 1 < Cfg::TN) next[it] = fetch((nt + 1) * 8 + it);
         const int n = wn * WN + nt * 32 + t;
@@ -345,7 +369,7 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
   if constexpr (kBwd) {
     if (fin.sums == nullptr) return;   // the same in all waves
     // over the wave's four tokens at a time, then over the waves side by side
-    float* const all = reinterpret_cast<float*>(smem);   // [WAVES_N][BM]
+    float* const all = reinterpret_cast<float*>(base);   // [kGroups][WAVES_N][BM]
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       sums[e] += __shfl_xor(sums[e], 16);
@@ -354,12 +378,12 @@ __device__ __forceinline__ void spmm_act_tile(unsigned char* __restrict__ smem, 
     __syncthreads();
     if (lane < 16)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) all[wn * BM + wm * WM + 8 * q + e] = sums[e];
+      for (int e = 0; e < 8; ++e) all[(group * Cfg::WAVES_N + wn) * BM + wm * WM + 8 * q + e] = sums[e];
     __syncthreads();
-    for (int c = tid; c < BM; c += Cfg::THREADS) {
+    for (int c = thread; c < BM; c += kGroups * kThreads) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < Cfg::WAVES_N; ++w) v += all[w * BM + c];
+      for (int w = 0; w < kGroups * Cfg::WAVES_N; ++w) v += all[w * BM + c];
       if (m0 + c < N) fin.sums[t0 / BN * N + m0 + c] = v;
     }
   }
@@ -377,17 +401,14 @@ __device__ __forceinline__ void tile_at(int lin, int tiles_m, int tiles_n, int& 
 
 // The tile's tokens are a matrix of their own to it, so that the direct loads'
 // 32-bit offsets count from its first row however many tokens there are.
-template <int BM, int BN, int WM, int WN, int kSlots, bool kBwd, bool kTail>
+template <int BM, int BN, int WM, int WN, int kSlots, int kGroups, bool kBwd, bool kTail>
 __device__ __forceinline__ void spmm_act_at(unsigned char* smem, const uint16_t* A, const uint16_t* vals,
                                             const uint16_t* meta, int64_t T, int64_t N, int64_t K, const Finish& fin,
                                             int tm, int tn) {
   const int64_t t0 = (int64_t)tn * BN;
-  spmm_act_tile<BM, BN, WM, WN, kSlots, kBwd, kTail>(smem, A + t0 * K, vals, meta, T - t0 < BN ? T - t0 : BN, N, K, tm, 0,
-                                                     (int)threadIdx.x, fin, t0);
+  spmm_act_tile<BM, BN, WM, WN, kSlots, kGroups, kBwd, kTail>(smem, A + t0 * K, vals, meta, T - t0 < BN ? T - t0 : BN, N, K,
+                                                              tm, 0, (int)threadIdx.x, fin, t0);
 }
-
-template <int BM, int BN>
-constexpr int tile_bytes(int slots) { return slots * (BM * 72 + BN * 128); }
 
 // 256 x 128 tiles of the first `big` x 256 features and 128 x 128 tiles of the
 // others, after them: the last, partly filled round of workgroups takes half as
@@ -408,13 +429,13 @@ __global__ __launch_bounds__(256, 2) void spmm_large_kernel(const uint16_t* __re
     const int lin = x * big_per_xcd + at;
     if (lin >= nbig) return;
     tile_at(lin, big, tiles_n, tm, tn);
-    spmm_act_at<256, 128, 128, 64, 2, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, tm, tn);
+    spmm_act_at<256, 128, 128, 64, 2, 1, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, tm, tn);
   } else {
     const int small = (int)((N - big * 256 + 127) / 128), nsmall = small * tiles_n, per_xcd = (nsmall + 7) / 8;
     const int lin = x * per_xcd + at - big_per_xcd;
     if (at - big_per_xcd >= per_xcd || lin >= nsmall) return;
     tile_at(lin, small, tiles_n, tm, tn);
-    spmm_act_at<128, 128, 128, 32, 2, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, 2 * big + tm, tn);
+    spmm_act_at<128, 128, 128, 32, 2, 1, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, 2 * big + tm, tn);
   }
 }
 
@@ -434,30 +455,32 @@ hipError_t launch_large(const uint16_t* A, const uint16_t* vals, const uint16_t*
   return hipGetLastError();
 }
 
-// 128 x 128 tiles throughout, with a three-slot ring.
-template <bool kBwd, bool kTail>
-__global__ __launch_bounds__(256, 2) void spmm_small_kernel(const uint16_t* __restrict__ A,
+// 128 x 128 tiles throughout, with a three-slot ring: two workgroups a CU, or, for
+// no more tiles than CUs, one of two groups of waves, which halves the chain of
+// stages (0.4 us each).
+template <int kGroups, bool kBwd, bool kTail>
+__global__ __launch_bounds__(256 * kGroups, 2 / kGroups) void spmm_small_kernel(const uint16_t* __restrict__ A,
                                                             const uint16_t* __restrict__ vals,
                                                             const uint16_t* __restrict__ meta, int64_t T, int64_t N,
                                                             int64_t K, Finish fin, int tiles_m, int tiles_n) {
-  __shared__ __align__(1024) unsigned char smem[tile_bytes<128, 128>(3)];
+  __shared__ __align__(1024) unsigned char smem[kGroups * tile_bytes<128, 128>(3)];
   const int ntiles = tiles_m * tiles_n, per_xcd = (ntiles + 7) / 8;
   const int lin = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
   if (lin >= ntiles) return;
   int tm, tn;
   tile_at(lin, tiles_m, tiles_n, tm, tn);
-  spmm_act_at<128, 128, 128, 32, 3, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, tm, tn);
+  spmm_act_at<128, 128, 128, 32, 3, kGroups, kBwd, kTail>(smem, A, vals, meta, T, N, K, fin, tm, tn);
 }
 
-template <bool kBwd>
+template <int kGroups, bool kBwd>
 hipError_t launch_small(const uint16_t* A, const uint16_t* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K,
                         const Finish& f, hipStream_t s) {
   const int tiles_m = (int)((N + 127) / 128), tiles_n = (int)((T + 127) / 128);
-  const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8)), block(256);
+  const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8)), block(256 * kGroups);
   if (K % 64 == 0)
-    hipLaunchKernelGGL((spmm_small_kernel<kBwd, false>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n);
+    hipLaunchKernelGGL((spmm_small_kernel<kGroups, kBwd, false>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n);
   else
-    hipLaunchKernelGGL((spmm_small_kernel<kBwd, true>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n);
+    hipLaunchKernelGGL((spmm_small_kernel<kGroups, kBwd, true>), grid, block, 0, s, A, vals, meta, T, N, K, f, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
@@ -683,7 +706,7 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const float* __restrict
 // How a product is run, by its sizes alone: the order of its sums does not depend
 // on the device.
 struct Plan {
-  enum { kThin, kMid, kSmall, kLarge } how;
+  enum { kThin, kMid, kPairs, kSmall, kLarge } how;
   int parts;       // of kMid
   int64_t block;   // tokens of one row of a backward's partial sums
   int64_t rows(int64_t T) const { return (T + block - 1) / block; }
@@ -699,12 +722,13 @@ Plan plan_product(int64_t T, int64_t N, int64_t K) {
   constexpr int64_t kMaxBuf = (int64_t)1 << 31;
   const bool fits = K >= 64 && K * 512 < kMaxBuf && N * K < kMaxBuf && tiles(64, 64) < ((int64_t)1 << 22);
   if (!fits || T <= 16 || (T <= 32 && K <= 1024)) return {Plan::kThin, 1, T <= 16 ? 16 : T <= 32 ? 32 : kThinTokens};
-  if (2 * tiles(64, 64) <= 3 * kCus) {
+  if (tiles(64, 64) <= kCus) {
     const int64_t rounds = (K / 64 + 3) / 4, parts = std::min(kCus / tiles(64, 64), rounds / 2);
     // the joining launch costs about 3 us, a round 0.47
     if (parts > 1 && rounds - (rounds + parts - 1) / parts >= 7) return {Plan::kMid, (int)parts, kJoinTokens};
     return {Plan::kMid, 1, 64};
   }
+  if (tiles(128, 128) <= kCus && K >= 128) return {Plan::kPairs, 1, 128};
   return {tiles(256, 128) < 2 * kCus ? Plan::kSmall : Plan::kLarge, 1, 128};
 }
 
@@ -713,7 +737,8 @@ hipError_t launch_product(const Plan& p, const uint16_t* A, const uint16_t* vals
                           int64_t N, int64_t K, const Finish& fin, float* ws, hipStream_t s) {
   switch (p.how) {
     case Plan::kThin: return launch_thin<kBwd>(A, vals, meta, T, N, K, fin, s);
-    case Plan::kSmall: return launch_small<kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kPairs: return launch_small<2, kBwd>(A, vals, meta, T, N, K, fin, s);
+    case Plan::kSmall: return launch_small<1, kBwd>(A, vals, meta, T, N, K, fin, s);
     case Plan::kLarge: return launch_large<kBwd>(A, vals, meta, T, N, K, fin, s);
     case Plan::kMid: break;
   }

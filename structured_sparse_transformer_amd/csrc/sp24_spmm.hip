@@ -256,7 +256,8 @@ __device__ __forceinline__ void spmm_fast_tile(unsigned char* __restrict__ smem,
                                                int64_t T, int64_t N, int64_t K, uint16_t* __restrict__ out,
                                                int64_t ldo, uint16_t* __restrict__ gout, int64_t ldg, int tm, int tn,
                                                int tid, bool post, int* post_dst, int post_val) {
-  constexpr int kSlots = 3;
+  constexpr int kSlots = 3, kt0 = 0;
+  const auto stages = [&] { return (int)(K / 64); };
 #include "sp24_spmm_loop.inc"
 
   // Epilogue: fp32 -> fp16 (round to nearest even).  Each wave stages its
