@@ -218,33 +218,38 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, ui
 // ---------------------------------------------------------------------------
 // AdamW.
 
-constexpr int kAdamTensors = 40;
 constexpr int64_t kAdamChunk = 4096;
+template <bool k8>
 struct AdamEntry {
   const void* G;
   float* P;
   void* M;
   void* V;
-  uint8_t* ME;
-  uint8_t* VE;
   uint16_t* W;
   int64_t n;
   float lr, keep;
+};
+template <>
+struct AdamEntry<true> : AdamEntry<false> {
+  uint8_t* ME;
+  uint8_t* VE;
   uint32_t place;
 };
+template <bool k8>
 struct AdamTable {
-  AdamEntry t[kAdamTensors];
-  uint32_t first[kAdamTensors];
+  static constexpr int kTensors = k8 ? 44 : 64;
+  AdamEntry<k8> t[kTensors];
+  uint32_t first[kTensors];
   int count;
   float b1, c1, b2, c2, eps, ln_b1, ln_b2;
   int64_t step;
   const Control* control;
   uint32_t seed;
 };
-static_assert(sizeof(AdamTable) <= 4000, "kernel arguments");
+static_assert(sizeof(AdamTable<true>) <= 4000 && sizeof(AdamTable<false>) <= 4000, "kernel arguments");
 
 template <bool kF16, bool k8>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable tab) {
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable<k8> tab) {
   int64_t step = tab.step;
   float factor = 1.0f;
   if (tab.control != nullptr) {
@@ -253,12 +258,13 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable tab) {
     factor = tab.control->factor;
   }
   const int k = tensor_of(tab.first, tab.count, blockIdx.x);
-  const AdamEntry& t = tab.t[k];
+  const AdamEntry<k8>& t = tab.t[k];
   const int64_t n = t.n, i0 = (int64_t)(blockIdx.x - tab.first[k]) * kAdamChunk;
   // 1 - b^step through expm1: the difference keeps its precision for b near 1
   const float rate = t.lr / -expm1f((float)step * tab.ln_b1);
   const float root = 1.0f / sqrtf(-expm1f((float)step * tab.ln_b2));
-  const uint32_t key = mix(mix(mix((uint32_t)step) ^ tab.seed) ^ t.place);
+  uint32_t key = 0;
+  if constexpr (k8) key = mix(mix(mix((uint32_t)step) ^ tab.seed) ^ t.place);
   // groups of 4 entries, kAhead of them under way at once
   constexpr int kGroups = kAdamChunk / (4 * kThreads), kAhead = k8 ? 4 : 2;
   static_assert(kGroups % kAhead == 0, "whole batches");
@@ -441,8 +447,10 @@ hipError_t launch_grad_norm(const void* const* grads, const int64_t* sizes, int6
   return hipGetLastError();
 }
 
-hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, bool state8, const AdamwParams& prm, hipStream_t s) {
-  AdamTable tab;
+namespace {
+template <bool kF16, bool k8>
+hipError_t launch_adamw_of(const sp24_adamw_job* jobs, int64_t count, const AdamwParams& prm, hipStream_t s) {
+  AdamTable<k8> tab;
   tab.b1 = (float)prm.beta1;
   tab.c1 = (float)(1.0 - prm.beta1);
   tab.b2 = (float)prm.beta2;
@@ -457,11 +465,7 @@ hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, boo
   uint32_t chunks = 0;
   const auto flush = [&]() {
     if (tab.count == 0) return hipSuccess;
-    const dim3 grid(chunks), block(kThreads);
-    if (f16 && state8) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, s, tab);
-    else if (f16) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, s, tab);
-    else if (state8) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, s, tab);
-    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, s, tab);
+    hipLaunchKernelGGL((adamw_kernel<kF16, k8>), dim3(chunks), dim3(kThreads), 0, s, tab);
     tab.count = 0;
     chunks = 0;
     return hipGetLastError();
@@ -470,16 +474,34 @@ hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, boo
     const sp24_adamw_job& j = jobs[k];
     const int64_t c = chunks_of(j.n, kAdamChunk);
     if (c == 0) continue;
-    if (tab.count == kAdamTensors || chunks + c > kMaxGrid) {
+    if (tab.count == AdamTable<k8>::kTensors || chunks + c > kMaxGrid) {
       const hipError_t e = flush();
       if (e != hipSuccess) return e;
     }
-    tab.t[tab.count] = AdamEntry{j.G, j.P, j.M, j.V, j.M_exps, j.V_exps, static_cast<uint16_t*>(j.W),
-                                  j.n, j.lr, 1.0f - j.decay, (uint32_t)k};
+    AdamEntry<k8>& t = tab.t[tab.count];
+    t.G = j.G;
+    t.P = j.P;
+    t.M = j.M;
+    t.V = j.V;
+    t.W = static_cast<uint16_t*>(j.W);
+    t.n = j.n;
+    t.lr = j.lr;
+    t.keep = 1.0f - j.decay;
+    if constexpr (k8) {
+      t.ME = j.M_exps;
+      t.VE = j.V_exps;
+      t.place = (uint32_t)k;
+    }
     tab.first[tab.count++] = chunks;
     chunks += (uint32_t)c;
   }
   return flush();
+}
+}  // namespace
+
+hipError_t launch_adamw(const sp24_adamw_job* jobs, int64_t count, bool f16, bool state8, const AdamwParams& prm, hipStream_t s) {
+  if (f16) return state8 ? launch_adamw_of<true, true>(jobs, count, prm, s) : launch_adamw_of<true, false>(jobs, count, prm, s);
+  return state8 ? launch_adamw_of<false, true>(jobs, count, prm, s) : launch_adamw_of<false, false>(jobs, count, prm, s);
 }
 
 hipError_t launch_state8_values(const uint8_t* codes, const uint8_t* exps, int64_t n, bool root, bool bf16, void* out,

@@ -65,10 +65,10 @@ def test_bwd_input_act(sp):
 
 def test_bias_grad(sp):
     f, size = sp.lib().sp24_bias_grad, sp.lib().sp24_bias_grad_workspace
-    need = size(1000, 32)
+    need = size(5000, 32)
     assert need > 0 and size(0, 32) == 0 and size(1, 32) == 0
 
-    def call(dY=A, T=1000, R=32, dbias=A, ws=A, n=need):
+    def call(dY=A, T=5000, R=32, dbias=A, ws=A, n=need):
         return f(dY, T, R, dbias, ws, n, None)
 
     assert call(T=-1) == SHAPE and call(R=24) == SHAPE and call(R=-16) == SHAPE

@@ -262,13 +262,13 @@ def test_workspace(sp):
     """A call writes nothing past the workspace that it asked for."""
     T, R, C = 150, 528, 6416
     f, _, gen = weight(sp, R, C, 6)
-    X, dY, U = (torch.randn(T, n, generator=gen, device="cuda").half() for n in (C, R, C))
+    X, dY, U, long = (torch.randn(t, n, generator=gen, device="cuda").half() for t, n in ((T, C), (T, R), (T, C), (2000, R)))
     for need, call in (
             (sp.lib().sp24_spmm_fwd_act_workspace(T, R, C),
              lambda w: sp.sp24_spmm_fwd_act(X, f["vals_row"], f["meta_row"], R, C, act="gelu", workspace=w)),
             (sp.lib().sp24_spmm_bwd_input_act_workspace(T, R, C),
              lambda w: sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], R, C, U, act="gelu", workspace=w)),
-            (sp.lib().sp24_bias_grad_workspace(T, R), lambda w: (sp.sp24_bias_grad(dY, workspace=w),))):
+            (sp.lib().sp24_bias_grad_workspace(2000, R), lambda w: (sp.sp24_bias_grad(long, workspace=w),))):
         assert need > 0
         ws = Guarded((need,), torch.uint8)
         got = call(ws.t)
@@ -278,7 +278,7 @@ def test_workspace(sp):
             call(ws.t[:need - 16])
 
 
-@pytest.mark.parametrize("T,R", [(1, 16), (1, 6400), (63, 48), (64, 512), (65, 528), (517, 1600), (4096, 1024),
+@pytest.mark.parametrize("T,R", [(1, 16), (1, 6400), (63, 48), (64, 512), (65, 528), (517, 1600), (1024, 80), (1025, 80), (4096, 1024),
                                  (16384, 6400), (100000, 16)])
 def test_bias_grad(sp, T, R):
     gen = torch.Generator(device="cuda").manual_seed(T + R)
