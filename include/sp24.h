@@ -606,7 +606,8 @@ enum {
  *   act            SP24_ACT_*
  *   residual  in   fp16 [T, R], or NULL
  *   U         out  fp16 [T, R], or NULL
- *   Y         out  fp16 [T, R]; may be the residual's own memory
+ *   Y         out  fp16 [T, R]; may be the residual's own memory (if that is not
+ *             X's too: other rows' products read X)
  *   workspace scratch device memory of sp24_spmm_fwd_act_workspace bytes (NULL
  *             where those are 0)
  * U of +inf gives +inf; of -inf 0 with RELU, RELU2 and GELU, NaN with GELU_TANH
@@ -656,8 +657,10 @@ int64_t sp24_spmm_bwd_input_act_workspace(int64_t T, int64_t R, int64_t C);
  *   dY        in   fp16 [T, R]
  *   T, R           >= 0, R a multiple of 16
  *   dbias     out  fp32 [R], written (zeros if T is 0)
- *   workspace scratch device memory of sp24_bias_grad_workspace bytes
- * Errors: NULL, SHAPE, ALIGN, TOO_LARGE, WORKSPACE, LAUNCH.
+ *   workspace scratch device memory of sp24_bias_grad_workspace bytes (NULL where
+ *             those are 0)
+ * Errors: NULL, SHAPE, ALIGN, WORKSPACE, LAUNCH; TOO_LARGE when T reaches 2^31,
+ * R 2^27 or dY 2^40 entries.
  */
 int sp24_bias_grad(const void* dY, int64_t T, int64_t R, float* dbias, void* workspace, int64_t workspace_bytes,
                    void* stream);
@@ -708,7 +711,7 @@ int64_t sp24_grad_norm_workspace(const int64_t* sizes, int64_t count);
  *   M <- beta1 M + (1 - beta1) g,   V <- beta2 V + (1 - beta2) g^2
  *   P <- (1 - decay) P - lr * (M / (1 - beta1^t)) / (sqrt(V / (1 - beta2^t)) + eps)
  *   W  = fp16(P)
- * Where control->skip is set, nothing is written.
+ * Where control->skip is set, or no step was counted yet, nothing is written.
  *
  * State type SP24_F32: M and V are fp32 [n].  SP24_STATE8: M and V are 8-bit
  * codes [n] with one exponent byte for every 64 consecutive entries, M_exps and

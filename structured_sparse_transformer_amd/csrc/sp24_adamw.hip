@@ -253,8 +253,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable<k8> tab) {
   int64_t step = tab.step;
   float factor = 1.0f;
   if (tab.control != nullptr) {
-    if (tab.control->skip != 0) return;
     step = tab.control->step;
+    if (tab.control->skip != 0 || step < 1) return;
     factor = tab.control->factor;
   }
   const int k = tensor_of(tab.first, tab.count, blockIdx.x);

@@ -164,7 +164,8 @@ int ns_launch(const sp24::NsJob* d, int count, const sp24::NsParams& prm, void* 
   return launch_status(sp24::launch_newton_schulz(d, count, prm, workspace, as_stream(stream)));
 }
 
-// The products with an epilogue launch a workgroup of 512 for 16 features.
+// The products with an epilogue launch a workgroup of 512 for 16 features, the
+// bias gradient one of 1024 for 64.
 constexpr int64_t kMaxActFeatures = (int64_t)1 << 27;
 
 int check_spmm_act(const void* A, const void* vals, const uint16_t* meta, int64_t T, int64_t N, int64_t K, int act,
@@ -192,7 +193,7 @@ int check_bias_grad(int64_t T, int64_t R) {
   if (T < 0) return SP24_ERR_SHAPE;
   const int st = check_dims(R, 0, 16);
   if (st != SP24_OK) return st;
-  return T >= kMaxDim || (T != 0 && R >= kMaxElems / T) ? SP24_ERR_TOO_LARGE : SP24_OK;
+  return T >= kMaxDim || R >= kMaxActFeatures || (T != 0 && R >= kMaxElems / T) ? SP24_ERR_TOO_LARGE : SP24_OK;
 }
 
 // Entries of a tensor of the optimiser's calls: at most 2^22 chunks of 4096.

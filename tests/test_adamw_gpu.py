@@ -176,6 +176,30 @@ def test_factor_and_step_from_the_control(sp):
     assert all(torch.equal(x, y) for p, q in zip(a, b) for x, y in zip(p, q))
 
 
+def test_a_control_before_the_first_step(sp):
+    """No step counted yet: nothing is written (and no division by 1 - b^0)."""
+    P = torch.ones(100, device="cuda")
+    plan = sp.sp24_adamw_plan([P], [torch.ones(100, device="cuda")], [torch.ones(100, device="cuda")])
+    sp.sp24_adamw_step(plan, [torch.ones(100, device="cuda")], control=sp.step_control())
+    assert all((t == 1).all() for part in plan.tensors[:3] for t in part)
+
+
+def test_refusals_on_the_gpu(sp):
+    """What needs tensors on the GPU to be refused."""
+    P = torch.ones(100, device="cuda")
+    plan = sp.sp24_adamw_plan([P], [torch.zeros_like(P)], [torch.zeros_like(P)])
+    for bad in ([P.cpu()], [torch.ones(100, 2, device="cuda")[:, 0]], [P.double()], [P, P]):
+        with pytest.raises(ValueError):
+            sp.sp24_adamw_step(plan, bad, step=1)
+        with pytest.raises(ValueError):
+            sp.sp24_grad_norm([P.cpu()] if bad[0] is P else bad)
+    with pytest.raises(sp.Sp24Error):   # 4 bytes past a multiple of 16
+        sp.sp24_adamw_step(plan, [torch.ones(101, device="cuda")[1:]], step=1)
+    with pytest.raises(sp.Sp24Error):
+        sp.sp24_grad_norm([P], max_norm=0.0)
+    assert (P == 1).all()
+
+
 # ------------------------------------------------------------------ 8 bits
 
 def eight(sp, sizes, gen, steps=0):

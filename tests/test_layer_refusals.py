@@ -72,8 +72,8 @@ def test_bias_grad(sp):
         return f(dY, T, R, dbias, ws, n, None)
 
     assert call(T=-1) == SHAPE and call(R=24) == SHAPE and call(R=-16) == SHAPE
-    assert call(T=2 ** 31) == TOO_LARGE and call(R=2 ** 31) == TOO_LARGE and call(T=2 ** 30, R=2 ** 10) == TOO_LARGE
-    assert size(-1, 32) == -1 and size(4, 24) == -1 and size(2 ** 31, 16) == -1
+    assert call(T=2 ** 31) == TOO_LARGE and call(R=2 ** 27) == TOO_LARGE and call(T=2 ** 30, R=2 ** 10) == TOO_LARGE
+    assert size(1, 2 ** 27) == -1 and size(-1, 32) == -1 and size(4, 24) == -1 and size(2 ** 31, 16) == -1
     for k in ("dY", "dbias", "ws"):
         assert call(**{k: None}) == NULL and call(**{k: MIS}) == ALIGN
     assert call(n=need - 1) == WORKSPACE and call(R=0, dY=None, dbias=None, ws=None) == OK
