@@ -72,7 +72,8 @@ __device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, float4v v
 
 // ---------------------------------------------------------------------------
 // The norm.  Squares are summed in fp64: no finite gradients overflow, and the
-// sum is not finite only where an entry is not.
+// sum is not finite only where an entry is not.  20.5 M fp32 entries (82 MB) in 14.9
+// us, 5.5 TB/s, and 2 to 4 us for the joining of the workgroups' sums.
 
 constexpr int kNormTensors = 128;
 constexpr int64_t kNormChunk = 16384;
@@ -148,7 +149,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(const double* __restrict__ p
 // V is held as its root, for half the range, and both are rounded up or down
 // at random: with b2 = 0.999 a step moves a root by a 2000th, which rounding to
 // nearest among steps of a 32nd would drop for ever.  A root above zero stays
-// above zero, so that no entry's step is divided by eps alone.
+// above zero, so that no entry's step is divided by eps alone.  64 entries a group
+// are 16 lanes of four, a row of the lane moves: the maximum takes no LDS.
 
 constexpr int kFracM = 3, kFracV = 4;
 
@@ -216,7 +218,11 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, ui
 }
 
 // ---------------------------------------------------------------------------
-// AdamW.
+// AdamW.  States in 32 bits: 28 bytes an entry, 30 with an fp16 copy (20.5 M entries,
+// 615 MB: 107 us traced, 120 as timed from outside, against 125 for a copy's 4.9
+// TB/s).  In 8 bits: 16 an entry with an exponent for each 64 of both states (80.4 M
+// entries, 1.29 GB by the counters: 257 us, 5.0 TB/s).  48 biases of 1600 and 6400 are
+// a launch of 6.2 us.
 
 constexpr int64_t kAdamChunk = 4096;
 template <bool k8>

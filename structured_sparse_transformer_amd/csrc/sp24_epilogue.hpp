@@ -52,8 +52,8 @@ __device__ __forceinline__ float activate(float u) {
   if constexpr (kAct == kActRelu) return u < 0.0f ? 0.0f : u;
   if constexpr (kAct == kActRelu2) return u < 0.0f ? 0.0f : u * u;
   if constexpr (kAct == kActGelu) {
-    // x Phi(x) = max(x, 0) - a Phi(-a)
-    const float a = tail_argument(u);
+    // x Phi(x) = max(x, 0) - a Phi(-a), NaN by the first part
+    const float a = __builtin_amdgcn_fmed3f(__builtin_fabsf(u), 0.0f, 10.0f);
     return __builtin_fmaf(-a, normal_tail(a), u < 0.0f ? 0.0f : u);
   }
   if constexpr (kAct == kActGeluTanh) return u * tanh_form(u, u * u);

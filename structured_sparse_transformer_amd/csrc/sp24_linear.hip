@@ -85,6 +85,10 @@ __device__ __forceinline__ void finish4(const Finish& fin, int64_t at, int64_t f
 // 4g .. 4g + 3.  Every byte of S is used by one wave, so S goes from memory
 // straight to registers.  The waves of a workgroup share the reduction out by
 // blocks and join their sums in LDS, in the order of the waves.
+//
+// 6400 x 1600 (11.5 MB of weight, 2.3 us at a copy's rate): 4.5 us for one token, 6.1
+// for 16; 1600 x 6400, 100 workgroups: 5.8 and 9.7.  Four blocks' loads under way at
+// once are slower (one token 4.2 -> 4.8), 4 or 16 waves no faster.
 template <int NT, int WAVES, bool kBwd>
 __global__ __launch_bounds__(64 * WAVES) void spmm_thin_kernel(const uint16_t* __restrict__ A,
                                                                const uint16_t* __restrict__ vals,
@@ -471,6 +475,7 @@ __global__ __launch_bounds__(256 * kGroups, 2 / kGroups) void spmm_small_kernel(
                                                             const uint16_t* __restrict__ meta, int64_t T, int64_t N,
                                                             int64_t K, Finish fin, int tiles_m, int tiles_n) {
   __shared__ __align__(1024) unsigned char smem[kGroups * tile_bytes<128, 128>(3)];
+  static_assert(sizeof(smem) >= kGroups * 4 * 16384, "the staging");
   const int ntiles = tiles_m * tiles_n, per_xcd = (ntiles + 7) / 8;
   const int lin = (int)(blockIdx.x % 8) * per_xcd + (int)(blockIdx.x / 8);
   if (lin >= ntiles) return;
@@ -501,7 +506,8 @@ hipError_t launch_small(const uint16_t* A, const uint16_t* vals, const uint16_t*
 // groups of four; group k sums up the stages k, k + 4, k + 8, ... of the whole
 // tile, 32 x 32 a wave, through a ring of its own, so that four stages are under
 // way in each CU and a quarter as many follow one another; and the tiles are a
-// quarter as large.  The four sums meet in LDS, in order.
+// quarter as large.  The four sums meet in LDS, in order.  (6400 x 1600 at 64 tokens:
+// 15.3 us thin, 8.0 here; 1600 x 6400 at 512: 41.9 in 128 x 128 tiles, 22.2.)
 //
 // With few tokens there are too few tiles even so, and a CU's loads are the
 // bound (51 KB a round of stages in 0.47 us, 52 bytes a cycle): `parts`
@@ -711,7 +717,18 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const float* __restrict
 }
 
 // How a product is run, by its sizes alone: the order of its sums does not depend
-// on the device.
+// on the device.  Where the choices change places (us in kernels; weights as
+// features x reduction):
+//   thin up to 16 tokens: 4096 x 1024 at 16 tokens 3.7, mid 6.2; 6400 x 1600 6.1 and
+//     7.5.  Up to 32 where the reduction is short: 4096 x 1024 at 32 4.7 and 6.3, but
+//     6400 x 1600 at 24 8.1 and 7.6.
+//   mid while there is a tile a CU at most: 1024 x 4096 at 1024 tokens (256 tiles) 15.7,
+//     pairs 24.7; 6400 x 1600 at 192 (300 tiles) 15.3 and 13.6.
+//   parts of a reduction: 1600 x 6400 at 24 tokens 17.1 in one part, 9.1 in 10.
+//   pairs while there is a tile a CU at most: 1024 x 4096 at 2048 tokens (128 tiles)
+//     25.6, small 30.7; 6400 x 1600 at 768 (300 tiles) 28.0 and 24.8.
+//   small while 256 x 128 tiles are fewer than the CUs: 1600 x 6400 at 4096 tokens
+//     (224) 75.9, large 79.4; 6400 x 1600 at 1500 (300) 38.9 and 34.4.
 struct Plan {
   enum { kThin, kMid, kPairs, kSmall, kLarge } how;
   int parts;       // of kMid
@@ -736,7 +753,7 @@ Plan plan_product(int64_t T, int64_t N, int64_t K) {
     return {Plan::kMid, 1, 64};
   }
   if (tiles(128, 128) <= kCus && K >= 128) return {Plan::kPairs, 1, 128};
-  return {tiles(256, 128) < 2 * kCus ? Plan::kSmall : Plan::kLarge, 1, 128};
+  return {tiles(256, 128) < kCus ? Plan::kSmall : Plan::kLarge, 1, 128};
 }
 
 template <bool kBwd>

@@ -13,7 +13,7 @@ import pytest
 CUS = 256
 SIZES = [(1, 6400, 1600), (17, 1600, 6400), (24, 1600, 6400), (33, 16, 16), (64, 112, 6400), (65, 1024, 320), (127, 64, 1616),
          (150, 528, 6416), (192, 6400, 1600), (257, 272, 128), (512, 1600, 6400), (1021, 4096, 1024), (1000, 128, 48),
-         (2500, 528, 656), (8192, 2064, 336), (16384, 6400, 1600), (16384, 1600, 6400), (70000, 64, 6400), (350000, 6400, 64)]
+         (2500, 528, 656), (8192, 2064, 336), (1500, 6400, 1600), (2048, 4096, 1024), (3000, 1600, 6400), (16384, 6400, 1600), (16384, 1600, 6400), (70000, 64, 6400), (350000, 6400, 64)]
 
 
 def cdiv(a, b):
@@ -33,7 +33,7 @@ def plan(T, N, K):
         return "mid", 1, 64
     if tiles(128, 128) <= CUS and K >= 128:
         return "pairs", 1, 128
-    return "small" if tiles(256, 128) < 2 * CUS else "large", 1, 128
+    return "small" if tiles(256, 128) < CUS else "large", 1, 128
 
 
 def tile_at(lin, tiles_m, tiles_n):
