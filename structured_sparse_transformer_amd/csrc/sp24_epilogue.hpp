@@ -61,11 +61,11 @@ __device__ __forceinline__ float activate(float u) {
   return u;
 }
 
-// d act'(u)
+// d act'(u).  RELU passes d where u is NaN: the forward's output is NaN there.
 template <int kAct>
 __device__ __forceinline__ float times_slope(float d, float u) {
-  if constexpr (kAct == kActRelu) return u > 0.0f ? d : 0.0f;
-  if constexpr (kAct == kActRelu2) return u > 0.0f ? d * (2.0f * u) : 0.0f;
+  if constexpr (kAct == kActRelu) return u <= 0.0f ? 0.0f : d;
+  if constexpr (kAct == kActRelu2) return u <= 0.0f ? 0.0f : d * (2.0f * u);
   if constexpr (kAct == kActGelu) {
     // Phi(x) + x phi(x): Phi(-a) - a phi(a) on the left, 1 less that on the right
     const float a = tail_argument(u);

@@ -228,6 +228,32 @@ def test_infinite_and_nan(sp):
         assert math.isnan(got[1]) if math.isnan(low) else got[1] == low
 
 
+def test_slopes_at_infinities_and_nan(sp):
+    """What the backward makes of U where the forward gave inf or NaN: no NaN of U
+    is lost, and no infinity turns one activation's limit into another's."""
+    R, C = 64, 64
+    f, Ws, gen = weight(sp, R, C, 9)
+    for T in (3, 40, 40000):   # thin, shared and whole tiles
+        dY = torch.ones(T, R, dtype=torch.float16, device="cuda")
+        U = torch.zeros(T, C, dtype=torch.float16, device="cuda")
+        U[:, 0], U[:, 1], U[:, 2] = math.nan, math.inf, -math.inf
+        d, _ = sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], R, C, None)
+        assert torch.isfinite(d).all() and (d[0, :3] != 0).all()
+        for act in ACTS[1:]:
+            got, db = sp.sp24_spmm_bwd_input_act(dY, f["vals_col"], f["meta_col"], R, C, U, act=act)
+            if act == "relu":
+                assert torch.equal(got[:, 0], d[:, 0])
+            else:
+                assert torch.isnan(got[:, 0]).all() and torch.isnan(db[0])
+            if act in ("relu", "gelu"):
+                assert torch.equal(got[:, 1], d[:, 1]) and (got[:, 2] == 0).all()
+            elif act == "relu2":
+                assert torch.isinf(got[:, 1]).all() and (got[:, 2] == 0).all()
+            else:
+                assert torch.isnan(got[:, 1:3]).all()
+            assert torch.isfinite(got[:, 3:]).all() and torch.isfinite(db[3:]).all()
+
+
 def test_no_tokens_and_no_width(sp):
     f, _, _ = weight(sp, 64, 32, 2)
     Y, U = sp.sp24_spmm_fwd_act(torch.empty(0, 32, dtype=torch.float16, device="cuda"), f["vals_row"], f["meta_row"], 64,
