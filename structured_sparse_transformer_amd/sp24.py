@@ -827,6 +827,10 @@ def sp24_adamw_plan(Ps, Ms, Vs, Ws=None, lrs=1e-3, decays=0.0, M_exps=None, V_ex
         if state8:
             _need(M_exps[k], (-(-sizes[k] // 64),), torch.uint8, "M_exps")
             _need(V_exps[k], (-(-sizes[k] // 64),), torch.uint8, "V_exps")
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for part in (Ps, Ms, Vs, Ws, *more)
+                   for t in part if t is not None and t.numel())
+    if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+        raise ValueError("tensors of a plan share memory: a tensor takes one step, whichever layers use it")
     ptr = lambda t: _ptr(t).value if t is not None and t.numel() else None  # noqa: E731
     jobs = (AdamwJob * n)(*[
         AdamwJob(None, ptr(Ps[k]), ptr(Ms[k]), ptr(Vs[k]), ptr(M_exps[k]) if state8 else None,

@@ -174,3 +174,17 @@ def test_binding(sp):
         sp.sp24_adamw_step(plan, [P[:3]], step=1)
     with pytest.raises(ValueError):
         sp.sp24_state8_values(c, e[:1])
+
+
+def test_a_plan_takes_no_memory_twice(sp):
+    """A tied weight listed twice, one state for two tensors, or parts of one
+    buffer that overlap: two workgroups would write the same entries."""
+    P, M, V, Q, N, U = (torch.zeros(70) for _ in range(6))
+    both = torch.zeros(139)
+    for args in (([P, P], [M, N], [V, U]), ([P, Q], [M, M], [V, U]), ([P], [M], [M]), ([P], [P], [V]),
+                 ([both[:70], both[69:]], [M, N], [V, U])):
+        with pytest.raises(ValueError, match="share memory"):
+            sp.sp24_adamw_plan(*args)
+    c, d, e = (torch.zeros(70, dtype=torch.uint8) for _ in range(3))
+    with pytest.raises(ValueError, match="share memory"):
+        sp.sp24_adamw_plan([P], [c], [d], M_exps=[e[:2]], V_exps=[e[1:3]])
