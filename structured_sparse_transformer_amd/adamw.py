@@ -59,12 +59,13 @@ class AdamW:
     def step(self, grads) -> None:
         """One step with the gradients of all tensors, in their order (all fp32 or
         all fp16)."""
+        # before any count goes on
+        if [g.numel() for g in grads] != self.plan.sizes:
+            raise ValueError("one gradient per tensor, of its size")
         if not self.guarded:
+            sp24.sp24_adamw_step(self.plan, grads, self.betas, self.eps, step=self.steps + 1, seed=self.seed)
             self.steps += 1
-            sp24.sp24_adamw_step(self.plan, grads, self.betas, self.eps, step=self.steps, seed=self.seed)
             return
-        if len(grads) != len(self.params):   # before the count goes on
-            raise ValueError("one gradient per tensor")
         sp24.sp24_grad_norm(grads, 1.0 / self.loss_scale, float("inf") if self.max_norm is None else self.max_norm,
                             control=self.control, workspace=self._work)
         sp24.sp24_adamw_step(self.plan, grads, self.betas, self.eps, control=self.control, seed=self.seed)

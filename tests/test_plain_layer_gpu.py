@@ -139,6 +139,21 @@ def test_optimiser(sp, bits, guard):
             assert w is None or torch.equal(w, p.half())
 
 
+@pytest.mark.parametrize("guard", [{}, {"max_norm": 1.0}])
+def test_a_refused_step_is_not_counted(sp, guard):
+    from structured_sparse_transformer_amd.adamw import AdamW
+    P = [torch.zeros(70, device="cuda"), torch.zeros(5, 3, device="cuda")]
+    optimizer = AdamW(P, **guard)
+    good = [torch.ones_like(p) for p in P]
+    for bad in (good[:1], [good[0], good[1][:4]], [good[0], good[1].half()], [g.cpu() for g in good], good[::-1]):
+        with pytest.raises(ValueError):
+            optimizer.step(bad)
+    steps = lambda: int(sp.control_values(optimizer.control)["step"]) if guard else optimizer.steps  # noqa: E731
+    assert steps() == 0 and not any(p.any() for p in P)
+    optimizer.step(good)
+    assert steps() == 1 and all(p.all() for p in P)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_step_captured_and_replayed(sp, bits):
     """Whole steps, tokens to new weights, captured and replayed over new tokens
