@@ -12,7 +12,7 @@ optionally an fp16 copy W that the products take.  A step does, in place,
 With a loss scale or a largest norm, t and the gradients' factor stay in device
 memory: a step whose gradients are not all finite is left out (and t with it)
 without the host's waiting for it, and a captured step counts on as it is
-replayed.
+replayed.  Without either, t is counted here and a step is not captured.
 """
 from __future__ import annotations
 
@@ -63,6 +63,8 @@ class AdamW:
         if [g.numel() for g in grads] != self.plan.sizes:
             raise ValueError("one gradient per tensor, of its size")
         if not self.guarded:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a captured step would replay its t: with a max_norm (infinity clips nothing) it counts on")
             sp24.sp24_adamw_step(self.plan, grads, self.betas, self.eps, step=self.steps + 1, seed=self.seed)
             self.steps += 1
             return

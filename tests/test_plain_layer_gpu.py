@@ -154,6 +154,34 @@ def test_a_refused_step_is_not_counted(sp, guard):
     assert steps() == 1 and all(p.all() for p in P)
 
 
+def test_a_captured_step_counts_on(sp):
+    """Refused where t would be a constant of the graph; with no more than an
+    infinite max_norm it counts, and gives the eager steps' bits."""
+    from structured_sparse_transformer_amd.adamw import AdamW
+    ends = []
+    G = [torch.ones(70, device="cuda")]
+    for how in ("eager", "captured", "plain"):
+        P = [torch.zeros(70, device="cuda")]
+        optimizer = AdamW(P, max_norm=None if how == "plain" else math.inf)
+        graph = torch.cuda.CUDAGraph()
+        if how == "plain":
+            with torch.cuda.graph(graph):
+                G[0].add_(0.0)
+                with pytest.raises(RuntimeError, match="captured"):
+                    optimizer.step(G)
+            assert optimizer.steps == 0
+            continue
+        if how == "captured":
+            with torch.cuda.graph(graph):
+                optimizer.step(G)
+        for _ in range(4):
+            graph.replay() if how == "captured" else optimizer.step(G)
+            torch.cuda.synchronize()
+        assert int(sp.control_values(optimizer.control)["step"]) == 4
+        ends.append(P[0])
+    assert torch.equal(*ends)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_a_step_captured_and_replayed(sp, bits):
     """Whole steps, tokens to new weights, captured and replayed over new tokens
