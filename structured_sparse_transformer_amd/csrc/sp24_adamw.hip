@@ -286,9 +286,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable<k8> tab) {
       if constexpr (k8) {
         mc[u] = load_codes(static_cast<const uint8_t*>(t.M), i, n);
         vc[u] = load_codes(static_cast<const uint8_t*>(t.V), i, n);
-        const int64_t group = (i < n ? i : 0) / 64;
-        me[u] = t.ME[group];
-        ve[u] = t.VE[group];
+        // lanes past the end have zeros for codes and exponents: another group's
+        // exponent may be 255, NaN for every code, and is its own row's to write
+        me[u] = i < n ? t.ME[i / 64] : 0;
+        ve[u] = i < n ? t.VE[i / 64] : 0;
       } else {
         m[u] = load4<false>(t.M, i, n);
         v[u] = load4<false>(t.V, i, n);
