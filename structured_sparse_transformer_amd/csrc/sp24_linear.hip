@@ -570,15 +570,17 @@ __global__ __launch_bounds__(1024, 1) void spmm_mid_kernel(const uint16_t* __res
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
 
-  // Stage j is issued two rounds ahead, into the slot that round j - 3 read:
-  // every wave is past the barrier of round j - 2 then.
+  // Stage j is issued two rounds ahead, into the slot that round j - 3 read: every
+  // wave is past the barrier of round j - 2 then, before which it has waited for
+  // the reads of round j - 3.
   if (mine > 0) issue(0);
   if (mine > 1) issue(1);
   for (int j = 0; j < rounds; ++j) {
-    // stage j has landed (the next one's 4 loads may be under way); vmcnt in
-    // bits 3:0, no wait for others
-    if (j + 1 < mine) __builtin_amdgcn_s_waitcnt(4 | (7 << 4) | (15 << 8));
-    else __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
+    // stage j has landed (the next one's 4 loads may be under way; vmcnt in bits
+    // 3:0), and this wave's LDS reads of round j - 1 are complete, whose slot the
+    // waves past the barrier overwrite (lgkmcnt, bits 11:8, 0); expcnt 7: no wait
+    if (j + 1 < mine) __builtin_amdgcn_s_waitcnt(4 | (7 << 4) | (0 << 8));
+    else __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (0 << 8));
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
