@@ -9,6 +9,9 @@ optionally an fp16 copy W that the products take.  A step does, in place,
     P <- (1 - lr weight_decay) P - lr (M / (1 - b1^t)) / (sqrt(V / (1 - b2^t)) + eps)
     W  = fp16(P)
 
+All of G carries the loss scale, what was added to the loss's own gradient (a
+layer's decay term) too.
+
 With a loss scale or a largest norm, t and the gradients' factor stay in device
 memory: a step whose gradients are not all finite is left out (and t with it)
 without the host's waiting for it, and a captured step counts on as it is

@@ -145,21 +145,24 @@ class SparseFFN(_TwoWeights):
         Y, U, H = self._products(X, True)
         return Y, Saved(X, U, H)
 
-    def backward(self, dY: torch.Tensor, saved: Saved):
+    def backward(self, dY: torch.Tensor, saved: Saved, loss_scale: float = 1.0):
         """dX, dW1, db1, dW2, db2.  dW2 and db2 run on a second stream beside dU
-        and dX, as in SparseGegluFFN."""
+        and dX, as in SparseGegluFFN.  ``loss_scale``: what the loss that dY is of
+        was multiplied with; the weights' decay term is too, so that the gradients
+        carry one scale throughout."""
         f1, f2 = self._current_forms()
         h, d = self.W1.shape
         main, side = self._streams()
         dW2 = torch.empty(d, h, dtype=torch.float32, device=dY.device)
         db2 = torch.empty(d, dtype=torch.float32, device=dY.device)
         work = torch.empty(sp24.lib().sp24_bias_grad_workspace(*dY.shape), dtype=torch.uint8, device=dY.device)
+        decay = self.decay * loss_scale
         dU, db1 = sp24.sp24_spmm_bwd_input_act(dY, f2["vals_col"], f2["meta_col"], d, h, saved.U, act=self.act)
         side.wait_stream(main)
-        sp24.sp24_weight_grad(dY, saved.Hg, self.W2, f2["idx"], self.decay, dW=dW2, stream=side)
+        sp24.sp24_weight_grad(dY, saved.Hg, self.W2, f2["idx"], decay, dW=dW2, stream=side)
         sp24.sp24_bias_grad(dY, dbias=db2, workspace=work, stream=side)
         # dU W1s + dY: the column form is the row form of the transpose
         dX, _ = sp24.sp24_spmm_fwd_act(dU, f1["vals_col"], f1["meta_col"], d, h, residual=dY if self.residual else None)
-        dW1 = sp24.sp24_weight_grad(dU, saved.X, self.W1, f1["idx"], self.decay)
+        dW1 = sp24.sp24_weight_grad(dU, saved.X, self.W1, f1["idx"], decay)
         main.wait_stream(side)
         return dX, dW1, db1, dW2, db2

@@ -61,7 +61,8 @@ class TokenFFN:
 
 class TokenMLP:
     """``table`` fp32 [V, d]; W1, b1, W2, b2 as SparseFFN takes them.  The fp32
-    masters of W1 and W2 start as their values.  ``adamw``: AdamW's arguments."""
+    masters of W1 and W2 start as their values.  ``decay`` is of the unscaled
+    gradients, whatever the loss scale.  ``adamw``: AdamW's arguments."""
 
     def __init__(self, table: torch.Tensor, W1: torch.Tensor, b1: torch.Tensor, W2: torch.Tensor, b2: torch.Tensor,
                  act: str = "gelu", scale: float = 1.0, decay: float = 0.0, **adamw):
@@ -80,8 +81,9 @@ class TokenMLP:
         return self.layer.forward(X)
 
     def backward(self, ids: torch.Tensor, dY: torch.Tensor, saved):
-        """The gradients of table, W1, b1, W2 and b2."""
-        dX, *grads = self.layer.backward(dY, saved)
+        """The gradients of table, W1, b1, W2 and b2, of the loss as dY is: multiplied
+        with the optimiser's loss_scale."""
+        dX, *grads = self.layer.backward(dY, saved, self.optimizer.loss_scale)
         return [sp24.sp24_embed_bwd(ids, dX, self.table.shape[0], self.scale), *grads]
 
     def update(self, grads) -> None:
