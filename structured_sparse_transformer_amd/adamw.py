@@ -60,11 +60,10 @@ class AdamW:
             job.lr, job.decay = lr, lr * w
 
     def step(self, grads) -> None:
-        """One step with the gradients of all tensors, in their order (all fp32 or
-        all fp16)."""
+        """One step with the gradients of all tensors, in their order and shapes
+        (all fp32 or all fp16)."""
         # before any count goes on
-        if [g.numel() for g in grads] != self.plan.sizes:
-            raise ValueError("one gradient per tensor, of its size")
+        self.plan.check(grads, [g.numel() for g in grads])
         if not self.guarded:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a captured step would replay its t: with a max_norm (infinity clips nothing) it counts on")

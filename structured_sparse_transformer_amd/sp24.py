@@ -795,10 +795,17 @@ class AdamwPlan:
 
     def __init__(self, jobs, tensors, sizes, state8):
         self.jobs, self.tensors, self.sizes, self.state8 = jobs, tensors, sizes, state8
+        self._shaped = [(k, P.shape) for k, P in enumerate(tensors[0]) if P.dim() > 1]
         self.address = ctypes.addressof(jobs) if sizes else None
         # the jobs' first fields, the gradients' addresses
         words = np.frombuffer(jobs, dtype=np.int64) if sizes else np.zeros(0, dtype=np.int64)
         self.gradients = words[::ctypes.sizeof(AdamwJob) // 8]
+
+    def check(self, Gs, sizes):
+        """That gradients of these sizes are the tensors'.  Not by sizes alone: the
+        gradients of [h, d] and [d, h] weights could be taken for one another."""
+        if sizes != self.sizes or any(Gs[k].shape != shape for k, shape in self._shaped):
+            raise ValueError("one gradient per tensor, of its shape")
 
 
 def sp24_adamw_plan(Ps, Ms, Vs, Ws=None, lrs=1e-3, decays=0.0, M_exps=None, V_exps=None):
@@ -840,13 +847,12 @@ def sp24_adamw_plan(Ps, Ms, Vs, Ws=None, lrs=1e-3, decays=0.0, M_exps=None, V_ex
 
 def sp24_adamw_step(plan, Gs, betas=(0.9, 0.999), eps=1e-8, step=None, control=None, seed=0, stream=None):
     """One AdamW step of a plan's tensors, in place, with the gradients ``Gs``
-    (all float16 or all float32): the ``step``-th (1, 2, ...), or as a control
-    that sp24_grad_norm wrote says."""
+    (all float16 or all float32, each of its tensor's shape): the ``step``-th (1,
+    2, ...), or as a control that sp24_grad_norm wrote says."""
     if (step is None) == (control is None):
         raise ValueError("either step or control")
     kind, pointers, sizes = _gradients(Gs)
-    if sizes != plan.sizes:
-        raise ValueError("one gradient per tensor, of its size")
+    plan.check(Gs, sizes)
     if pointers and plan.tensors[0][0].get_device() != Gs[0].get_device():
         raise ValueError("the plan's tensors are not on the current device")
     plan.gradients[:] = pointers
