@@ -33,10 +33,13 @@ class AdamW:
                  bits: int = 32, max_norm: float | None = None, loss_scale: float = 1.0, seed: int = 0):
         if bits not in (8, 32):
             raise ValueError("states are of 32 bits or of 8")
+        # here and not in the call, which comes after the norm has counted the step
+        if not all(0.0 <= b < 1.0 for b in betas) or not eps >= 0.0:
+            raise ValueError("betas must be from 0 up to below 1, eps 0 or more")
         self.params = list(params)
         n = len(self.params)
         self.copies = [None] * n if copies is None else list(copies)
-        self.betas, self.eps, self.seed = betas, eps, seed
+        self.betas, self.eps, self.seed = tuple(float(b) for b in betas), float(eps), int(seed)
         self.weight_decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
         if bits == 32:
             self.states = [(torch.zeros_like(p), torch.zeros_like(p)) for p in self.params]

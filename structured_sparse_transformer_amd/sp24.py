@@ -838,6 +838,9 @@ def sp24_adamw_plan(Ps, Ms, Vs, Ws=None, lrs=1e-3, decays=0.0, M_exps=None, V_ex
                    for t in part if t is not None and t.numel())
     if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
         raise ValueError("tensors of a plan share memory: a tensor takes one step, whichever layers use it")
+    # here, since a step that the library refuses comes after the norm has counted it
+    if any(t.data_ptr() % 16 for part in (Ps, Ms, Vs, Ws) for t in part if t is not None and t.numel()):
+        raise ValueError("tensors of a plan must be 16-byte aligned (all but the exponents)")
     ptr = lambda t: _ptr(t).value if t is not None and t.numel() else None  # noqa: E731
     jobs = (AdamwJob * n)(*[
         AdamwJob(None, ptr(Ps[k]), ptr(Ms[k]), ptr(Vs[k]), ptr(M_exps[k]) if state8 else None,
