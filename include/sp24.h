@@ -607,7 +607,8 @@ enum {
  *   residual  in   fp16 [T, R], or NULL
  *   U         out  fp16 [T, R], or NULL
  *   Y         out  fp16 [T, R]; may be the residual's own memory (if that is not
- *             X's too: other rows' products read X)
+ *             X's too: other rows' products read X).  Apart from that U and Y
+ *             share no memory with each other or with what the call reads.
  *   workspace scratch device memory of sp24_spmm_fwd_act_workspace bytes (NULL
  *             where those are 0)
  * U of +inf gives +inf; of -inf 0 with RELU, RELU2 and GELU, NaN with GELU_TANH
@@ -639,7 +640,9 @@ int64_t sp24_spmm_fwd_act_workspace(int64_t T, int64_t R, int64_t C);
  *   T, R, C        as sp24_spmm_fwd_act
  *   act            SP24_ACT_*; U may be NULL with SP24_ACT_NONE
  *   U         in   fp16 [T, C]
- *   dU        out  fp16 [T, C]; may be U's own memory
+ *   dU        out  fp16 [T, C]; may be U's own memory (if that is not dY's too).
+ *             Apart from that dU and dbias share no memory with each other or
+ *             with what the call reads.
  *   dbias     out  fp32 [C], or NULL.  Written, not accumulated (zeros if T is 0).
  *   workspace scratch device memory of sp24_spmm_bwd_input_act_workspace bytes
  *             (NULL where those are 0)

@@ -661,11 +661,27 @@ def _addresses(*tensors):
     return res
 
 
+def _apart(outputs, inputs, in_place):
+    """That the outputs which the caller passed share no memory with each other or
+    with what other workgroups of the call may still read; the first of them may be
+    the input `in_place` itself, where every entry is read and written by one lane."""
+    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())  # noqa: E731
+    given = [t for t in outputs if isinstance(t, torch.Tensor)]
+    for k, out in enumerate(given):
+        a, b = span(out)
+        own = in_place is not None and out is outputs[0] and a == in_place.data_ptr()
+        for t in (*given[:k], *inputs, None if own else in_place):
+            c, d = (0, 0) if t is None else span(t)
+            if a < d and c < b:
+                raise ValueError("an output shares memory with another tensor of the call")
+
+
 def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residual=None, U=False, out=None,
                       workspace=None, stream=None):
     """Y [T, R] = act(U) + residual, U = X * Ws^T + bias (float32 [R]); each
     rounded once to float16.  U=True also returns U (a tensor may be passed
-    instead); returns (Y, U or None).  ``out`` may be the residual."""
+    instead); returns (Y, U or None).  ``out`` may be the residual, unless that is
+    X; otherwise outputs share no memory with the call's other tensors."""
     kind, f16 = _act(act), torch.float16
     T = X.shape[0]
     if X.dtype != f16 or X.shape != (T, C):
@@ -675,6 +691,8 @@ def sp24_spmm_fwd_act(X, vals_row, meta_row, R, C, act="none", bias=None, residu
         _need(bias, (R,), torch.float32, "bias")
     if residual is not None and (residual.dtype != f16 or residual.shape != (T, R)):
         _need(residual, (T, R), f16, "residual")
+    if out is not None or isinstance(U, torch.Tensor):
+        _apart((out, U), (X, vals_row, meta_row, bias), residual)
     L = lib()
     with _using(stream):
         out = X.new_empty((T, R)) if out is None else _out(out, (T, R), f16, X.device)
@@ -693,7 +711,8 @@ def sp24_spmm_bwd_input_act(dY, vals_col, meta_col, R, C, U, act="none", dbias=T
     """dU [T, C] = (dY [T, R] * Ws) * act'(U) and dbias [C] (float32), dU's sums
     over tokens before they are rounded.  dbias=False leaves the sums out (a
     tensor may be passed instead).  ``out`` may be U, and U None without an
-    activation.  Returns (dU, dbias or None)."""
+    activation; otherwise outputs share no memory with the call's other tensors.
+    Returns (dU, dbias or None)."""
     kind, f16 = _act(act), torch.float16
     T = dY.shape[0]
     if dY.dtype != f16 or dY.shape != (T, R):
@@ -701,6 +720,8 @@ def sp24_spmm_bwd_input_act(dY, vals_col, meta_col, R, C, U, act="none", dbias=T
     _row_form(vals_col, meta_col, C, R, "the column form")
     if U is not None or kind:
         _need(U, (T, C), f16, "U")
+    if out is not None or isinstance(dbias, torch.Tensor):
+        _apart((out, dbias), (dY, vals_col, meta_col), U)
     L = lib()
     with _using(stream):
         out = _out(out, (T, C), f16, dY.device)
