@@ -740,6 +740,8 @@ int64_t sp24_grad_norm_workspace(const int64_t* sizes, int64_t count);
  *   beta1, beta2      0 <= beta < 1;  eps >= 0
  *   step              t >= 1 (not read with a control)
  *   control   in      one sp24_step_control in device memory, or NULL
+ * What the jobs hold, beta1, beta2, eps and seed are taken as the call is made: a
+ * captured call replays them, lr and decay too.
  * Pointers are 16-byte aligned, the exponents' at any byte.  The buffers of a
  * call may not overlap.
  * Errors: NULL, SHAPE (also step below 1), ALIGN, LAUNCH; UNSUPPORTED for

@@ -16,8 +16,14 @@ With a loss scale or a largest norm, t and the gradients' factor stay in device
 memory: a step whose gradients are not all finite is left out (and t with it)
 without the host's waiting for it, and a captured step counts on as it is
 replayed.  Without either, t is counted here and a step is not captured.
+
+Everything else of a captured step is a constant of its graph: the learning rate
+and the decay, betas, eps, the scale and the largest norm.  A replay after
+``set_lr`` still takes the rate that it was captured with; capture it again.
 """
 from __future__ import annotations
+
+import warnings
 
 import torch
 
@@ -52,6 +58,7 @@ class AdamW:
         self.max_norm, self.loss_scale = max_norm, float(loss_scale)
         self.guarded = max_norm is not None or self.loss_scale != 1.0
         self.steps = 0
+        self._captured = False
         device = self.params[0].device if n else torch.device("cuda", torch.cuda.current_device())
         self.control = sp24.step_control(device) if self.guarded else None
         # the norm's parts: the same for every step
@@ -59,6 +66,11 @@ class AdamW:
         self._work = torch.empty(sp24.lib().sp24_grad_norm_workspace(at, n), dtype=torch.uint8, device=device) if self.guarded else None
 
     def set_lr(self, lr: float) -> None:
+        """The learning rate of the steps from here on; those that were captured
+        before keep theirs, which is warned of."""
+        if self._captured:
+            warnings.warn("a captured step keeps its learning rate when it is replayed: capture it again", RuntimeWarning, stacklevel=2)
+            self._captured = False
         for job, w in zip(self.plan.jobs, self.weight_decay):
             job.lr, job.decay = lr, lr * w
 
@@ -67,8 +79,9 @@ class AdamW:
         (all fp32 or all fp16)."""
         # before any count goes on
         self.plan.check(grads, [g.numel() for g in grads])
+        capturing = torch.cuda.is_current_stream_capturing()
         if not self.guarded:
-            if torch.cuda.is_current_stream_capturing():
+            if capturing:
                 raise RuntimeError("a captured step would replay its t: with a max_norm (infinity clips nothing) it counts on")
             sp24.sp24_adamw_step(self.plan, grads, self.betas, self.eps, step=self.steps + 1, seed=self.seed)
             self.steps += 1
@@ -76,3 +89,4 @@ class AdamW:
         sp24.sp24_grad_norm(grads, 1.0 / self.loss_scale, float("inf") if self.max_norm is None else self.max_norm,
                             control=self.control, workspace=self._work)
         sp24.sp24_adamw_step(self.plan, grads, self.betas, self.eps, control=self.control, seed=self.seed)
+        self._captured |= capturing
