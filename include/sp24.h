@@ -737,7 +737,8 @@ int64_t sp24_grad_norm_workspace(const int64_t* sizes, int64_t count);
  *     n               >= 0
  *     lr, decay       the update's factor and the part of P that is taken off
  *                     (lr times the weight decay)
- *   beta1, beta2      0 <= beta < 1;  eps >= 0
+ *   beta1, beta2      0 <= beta < 1;  eps >= 0, rounded to fp32: if it is 0 there
+ *                     an entry whose V is 0 in fp32 is divided by 0
  *   step              t >= 1 (not read with a control)
  *   control   in      one sp24_step_control in device memory, or NULL
  * What the jobs hold, beta1, beta2, eps and seed are taken as the call is made: a

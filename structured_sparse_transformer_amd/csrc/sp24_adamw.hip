@@ -221,8 +221,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int64_t n, ui
 // AdamW.  States in 32 bits: 28 bytes an entry, 30 with an fp16 copy (20.5 M entries,
 // 615 MB: 107 us traced, 120 as timed from outside, against 125 for a copy's 4.9
 // TB/s).  In 8 bits: 16 an entry with an exponent for each 64 of both states (80.4 M
-// entries, 1.29 GB by the counters: 257 us, 5.0 TB/s).  48 biases of 1600 and 6400 are
-// a launch of 6.2 us.
+// entries, 1.29 GB by the counters: 252-257 us, 5.1 TB/s).  48 biases of 4096 and 1024
+// are a launch of 6.1 us.
 
 constexpr int64_t kAdamChunk = 4096;
 template <bool k8>
@@ -288,6 +288,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamTable<k8> tab) {
         vc[u] = load_codes(static_cast<const uint8_t*>(t.V), i, n);
         // lanes past the end have zeros for codes and exponents: another group's
         // exponent may be 255, NaN for every code, and is its own row's to write
+        // (1.5% slower than a load by all lanes of one: 242.5 and 238.7 us a step)
         me[u] = i < n ? t.ME[i / 64] : 0;
         ve[u] = i < n ? t.VE[i / 64] : 0;
       } else {

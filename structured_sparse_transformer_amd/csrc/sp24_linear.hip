@@ -507,7 +507,7 @@ hipError_t launch_small(const uint16_t* A, const uint16_t* vals, const uint16_t*
 // tile, 32 x 32 a wave, through a ring of its own, so that four stages are under
 // way in each CU and a quarter as many follow one another; and the tiles are a
 // quarter as large.  The four sums meet in LDS, in order.  (6400 x 1600 at 64 tokens:
-// 15.3 us thin, 8.0 here; 1600 x 6400 at 512: 41.9 in 128 x 128 tiles, 22.2.)
+// 15.3 us thin, 7.8 here; 1600 x 6400 at 512: 41.9 in 128 x 128 tiles, 20.6.)
 //
 // With few tokens there are too few tiles even so, and a CU's loads are the
 // bound (51 KB a round of stages in 0.47 us, 52 bytes a cycle): `parts`
@@ -721,12 +721,15 @@ __global__ __launch_bounds__(256) void join_parts_kernel(const float* __restrict
 // How a product is run, by its sizes alone: the order of its sums does not depend
 // on the device.  Where the choices change places (us in kernels; weights as
 // features x reduction):
-//   thin up to 16 tokens: 4096 x 1024 at 16 tokens 3.7, mid 6.2; 6400 x 1600 6.1 and
-//     7.5.  Up to 32 where the reduction is short: 4096 x 1024 at 32 4.7 and 6.3, but
-//     6400 x 1600 at 24 8.1 and 7.6.
+//   thin up to 16 tokens: 4096 x 1024 at 16 tokens 3.8, mid 6.2; 6400 x 1600 6.1 and
+//     7.5; 1024 x 4096 7.1 and 7.6.  The longest reductions change places earlier
+//     (1600 x 6400 at 8 tokens 7.8 and 8.6, at 12 8.8 and 8.6, at 16 9.8 and 8.7): one
+//     border for all of them costs those 12% at most.  Up to 32 where the reduction is
+//     short: 4096 x 1024 at 24 4.4 and 6.2, at 32 4.7 and 6.3, but 6400 x 1600 at 24 8.1
+//     and 7.6.
 //   mid while there is a tile a CU at most: 1024 x 4096 at 1024 tokens (256 tiles) 15.7,
 //     pairs 24.7; 6400 x 1600 at 192 (300 tiles) 15.3 and 13.6.
-//   parts of a reduction: 1600 x 6400 at 24 tokens 17.1 in one part, 9.1 in 10.
+//   parts of a reduction: 1600 x 6400 at 24 tokens 17.1 in one part, 9.0 in 10.
 //   pairs while there is a tile a CU at most: 1024 x 4096 at 2048 tokens (128 tiles)
 //     25.6, small 30.7; 6400 x 1600 at 768 (300 tiles) 28.0 and 24.8.
 //   small while 256 x 128 tiles are fewer than the CUs: 1600 x 6400 at 4096 tokens

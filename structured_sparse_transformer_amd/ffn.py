@@ -96,8 +96,8 @@ class SparseGegluFFN(_TwoWeights):
         return Y, Saved(X, U, Hg)
 
     def backward(self, dY: torch.Tensor, saved: Saved):
-        """dW2 runs on a second stream beside dHg, the GEGLU backward and dX,
-        which do not need it: its last round of tiles leaves most CUs to
+        """dW2 runs on a second stream once dHg is done, beside the GEGLU backward
+        and dX, which do not need it: its last round of tiles leaves most CUs to
         them.  The caller's stream waits for it before this returns, and
         every output is allocated on the caller's stream."""
         f1, f2 = self._current_forms()
@@ -146,8 +146,8 @@ class SparseFFN(_TwoWeights):
         return Y, Saved(X, U, H)
 
     def backward(self, dY: torch.Tensor, saved: Saved, loss_scale: float = 1.0):
-        """dX, dW1, db1, dW2, db2.  dW2 and db2 run on a second stream beside dU
-        and dX, as in SparseGegluFFN.  ``loss_scale``: what the loss that dY is of
+        """dX, dW1, db1, dW2, db2.  dW2 and db2 run on a second stream once dU is
+        done, beside dX and dW1.  ``loss_scale``: what the loss that dY is of
         was multiplied with; the weights' decay term is too, so that the gradients
         carry one scale throughout."""
         f1, f2 = self._current_forms()
