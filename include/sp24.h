@@ -629,7 +629,8 @@ int64_t sp24_spmm_fwd_act_workspace(int64_t T, int64_t R, int64_t C);
  *     dU = (dY * Ws) * act'(U),   dbias[c] = sum over t of dU[t][c]
  * The layer's input is act(U), U = its predecessor's products with their bias:
  * dU is the gradient that the predecessor's weight and input gradients take.
- * RELU's and RELU2's slope at 0 is 0; where U is NaN so is dU, but RELU's is the
+ * RELU's and RELU2's slope at 0 is 0, and where U <= 0 they give 0 whatever the
+ * product is, infinite and NaN ones too; where U is NaN so is dU, but RELU's is the
  * product alone.  U of an infinity: RELU, RELU2 and GELU have their limits, GELU_TANH
  * and SILU NaN.  fp32 throughout; the sums are of the
  * unrounded values, in an order that T, R and C fix, so the same call gives
